@@ -23,6 +23,17 @@ and _narrow C variants are reached through the dtype of the tensors passed):
     w4a8_kernel_name / w8a8_is_kernel_name / w4a8_moe_kernel_name -> kernel a shape runs
     set_prefill_kernel("auto" | "wide" | "tiled")   tile kernel of the W4A8 GEMMs for M > 64
     w4a8_workspace_bytes(M, N, K)          -> split-K workspace the integer-scale GEMM uses
+
+Mixture-of-experts routing and rows, and weight-only products of few rows:
+    moe_route(logits, k, norm="chosen")    -> (weights, ids, offs, tok, pos)
+    moe_route_backward(dweights, logits, ids, norm="chosen") -> dlogits
+    moe_sort(ids, E)                       -> (offs, tok, pos)
+    moe_gather(x, offs, pos)               -> xs     (rows in expert order)
+    moe_gather_backward(dxs, pos)          -> dx
+    moe_combine(ys, pos, weights)          -> y      (rows back to the tokens)
+    moe_combine_backward(dy, ys, offs, pos, weights) -> (dys, dweights)
+    w4a16_gemv(x, packed, fscale, N)       -> y
+    w4a16_moe_gemv(x, offs, tok, packed, fscale, N)  -> y
 """
 from __future__ import annotations
 
@@ -56,6 +67,9 @@ EXPORTED = (
     "bgt_pack_weights_int8", "bgt_w8a8_gemm_is", "bgt_w8a8_is_kernel_name",
     "bgt_w4a8_moe_gemm_is", "bgt_w4a8_moe_kernel_name", "bgt_repack_int4_canonical",
     "bgt_set_prefill_kernel", "bgt_w4a8_workspace_bytes", "bgt_w4a8_gemm_is_noalloc",
+    "bgt_moe_route", "bgt_moe_sort", "bgt_moe_sort_workspace_bytes", "bgt_moe_route_backward",
+    "bgt_moe_gather", "bgt_moe_combine", "bgt_moe_combine_backward", "bgt_w4a16_gemv",
+    "bgt_w4a16_moe_gemv",
 )
 _NAMES = ("bgt_status_string", "bgt_w4a8_kernel_name", "bgt_w8a8_is_kernel_name",
           "bgt_w4a8_moe_kernel_name")
@@ -104,9 +118,19 @@ def lib():
         L.bgt_set_prefill_kernel.argtypes = [I]
         L.bgt_w4a8_workspace_bytes.argtypes = [I64, I64, I64]
         L.bgt_w4a8_gemm_is_noalloc.argtypes = [P, P, P, P, I, I64, I64, I64, P, P, P]
+        L.bgt_moe_route.argtypes = [P, I, I64, I64, I64, I64, I, P, P, P, P, P, P, I64, P]
+        L.bgt_moe_sort.argtypes = [P, I64, I64, I64, P, P, P, P, I64, P]
+        L.bgt_moe_sort_workspace_bytes.argtypes = [I64, I64, I64]
+        L.bgt_moe_route_backward.argtypes = [P, P, I, I64, P, I64, I64, I64, I, P, P]
+        L.bgt_moe_gather.argtypes = [P, I, I64, P, P, I64, I64, I64, I64, P, P]
+        L.bgt_moe_combine.argtypes = [P, I, P, P, I64, I64, I64, P, P]
+        L.bgt_moe_combine_backward.argtypes = [P, I64, P, I, P, P, P, I64, I64, I64, I64, P, P, P]
+        L.bgt_w4a16_gemv.argtypes = [P, I, I64, P, P, I64, I64, I64, P, I, P]
+        L.bgt_w4a16_moe_gemv.argtypes = [P, I, I64, I64, P, P, I64, I64, P, P, I64, I64, P, I, P]
         for f in EXPORTED:
             getattr(L, f).restype = ctypes.c_char_p if f in _NAMES else I
         L.bgt_w4a8_workspace_bytes.restype = I64
+        L.bgt_moe_sort_workspace_bytes.restype = I64
         _lib = L
     return _lib
 
@@ -509,3 +533,207 @@ def w4a8_moe_gemm_is(qx, sx, offsets, slot_token, packed, iscale, alpha: int, N:
     _raise("bgt_w4a8_moe_gemm_is", st)
     return y
 
+
+# ------------------------------------------- mixture-of-experts routing and rows
+_NORMS = {"chosen": 0, "all": 1}
+
+
+def _rows(t, name):
+    """(rows, columns, row stride) of a 2-D GPU matrix with unit column stride."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2 \
+            or (t.stride(1) != 1 and t.shape[1] != 1):
+        raise ValueError(f"{name} must be a 2-D GPU tensor with unit column stride")
+    rows, cols = t.shape
+    return rows, cols, (t.stride(0) if rows > 1 else cols)
+
+
+def _norm(norm):
+    if norm not in _NORMS:
+        raise ValueError(f"norm must be one of {sorted(_NORMS)}")
+    return _NORMS[norm]
+
+
+def _sort_buffers(T, E, k, dev, offs, tok, pos):
+    """The sort's outputs (allocated where not given) and its workspace."""
+    torch = _torch()
+    need = lib().bgt_moe_sort_workspace_bytes(T, E, k)
+    _raise("bgt_moe_sort_workspace_bytes", need if need < 0 else 0)
+    offs = torch.empty(E + 1, dtype=torch.int32, device=dev) if offs is None else offs
+    tok = torch.empty(T * k, dtype=torch.int32, device=dev) if tok is None else tok
+    pos = torch.empty((T, k), dtype=torch.int32, device=dev) if pos is None else pos
+    _check(offs, "offs", torch.int32, (E + 1,))
+    _check(tok, "tok", torch.int32, (T * k,))
+    _check(pos, "pos", torch.int32, (T, k))
+    ws = torch.empty(need // 4, dtype=torch.int32, device=dev) if need else None
+    return offs, tok, pos, ws, need
+
+
+def moe_route(logits, k: int, norm: str = "chosen", weights=None, ids=None, offs=None, tok=None,
+              pos=None):
+    """The k experts of each token and the slots sorted by expert.
+
+    logits: T x E float32, float16 or bfloat16. The k largest are chosen, equal
+    ones by the lower expert; -inf and NaN never are. weights (T x k float32) is
+    the softmax over the chosen experts (norm "chosen") or over all ("all").
+    Returns (weights, ids, offs, tok, pos): ids (T x k int32, -1 where too few
+    experts were left), offs (E+1) and tok (T*k, -1 past offs[E]) as the grouped
+    products take them, pos (T x k) the sorted slot of each (token, expert)."""
+    torch = _torch()
+    T, E, ld = _rows(logits, "logits")
+    lt, nm, k, dev = _elem_type(logits, "logits"), _norm(norm), int(k), logits.device
+    offs, tok, pos, ws, need = _sort_buffers(T, E, k, dev, offs, tok, pos)
+    weights = torch.empty((T, k), dtype=torch.float32, device=dev) if weights is None else weights
+    ids = torch.empty((T, k), dtype=torch.int32, device=dev) if ids is None else ids
+    _check(weights, "weights", torch.float32, (T, k))
+    _check(ids, "ids", torch.int32, (T, k))
+    st = lib().bgt_moe_route(_ptr(logits), lt, ld, T, E, k, nm, _ptr(weights), _ptr(ids),
+                             _ptr(offs), _ptr(tok), _ptr(pos), _ptr(ws), need, _stream(dev))
+    _raise("bgt_moe_route", st)
+    return weights, ids, offs, tok, pos
+
+
+def moe_sort(ids, E: int, offs=None, tok=None, pos=None):
+    """The slots of ids (T x k int32; outside [0, E): dropped) sorted by expert.
+    Returns (offs, tok, pos) as moe_route does."""
+    torch = _torch()
+    _check(ids, "ids", torch.int32)
+    if ids.dim() != 2:
+        raise ValueError("ids must be 2-D")
+    T, k = ids.shape
+    offs, tok, pos, ws, need = _sort_buffers(T, int(E), k, ids.device, offs, tok, pos)
+    st = lib().bgt_moe_sort(_ptr(ids), T, int(E), k, _ptr(offs), _ptr(tok), _ptr(pos), _ptr(ws),
+                            need, _stream(ids.device))
+    _raise("bgt_moe_sort", st)
+    return offs, tok, pos
+
+
+def moe_route_backward(dweights, logits, ids, norm: str = "chosen", dlogits=None):
+    """Gradient of the logits (their dtype, T x E) from that of moe_route's weights."""
+    torch = _torch()
+    T, E, ld = _rows(logits, "logits")
+    lt, nm = _elem_type(logits, "logits"), _norm(norm)
+    _check(ids, "ids", torch.int32)
+    if ids.dim() != 2 or ids.shape[0] != T:
+        raise ValueError("ids must be T x k")
+    k = ids.shape[1]
+    _check(dweights, "dweights", torch.float32, (T, k))
+    if dlogits is None:
+        dlogits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    _check(dlogits, "dlogits", logits.dtype, (T, E))
+    st = lib().bgt_moe_route_backward(_ptr(dweights), _ptr(logits), lt, ld, _ptr(ids), T, E, k, nm,
+                                      _ptr(dlogits), _stream(logits.device))
+    _raise("bgt_moe_route_backward", st)
+    return dlogits
+
+
+def moe_gather(x, offs, pos, xs=None):
+    """Token rows (T x H) in expert order (T*k x H); slots past offs[-1] are zero."""
+    torch = _torch()
+    T, H, ld = _rows(x, "x")
+    xt = _elem_type(x, "x")
+    _check(offs, "offs", torch.int32)
+    _check(pos, "pos", torch.int32)
+    if pos.dim() != 2 or pos.shape[0] != T:
+        raise ValueError("pos must be T x k")
+    k = pos.shape[1]
+    xs = torch.empty((T * k, H), dtype=x.dtype, device=x.device) if xs is None else xs
+    _check(xs, "xs", x.dtype, (T * k, H))
+    st = lib().bgt_moe_gather(_ptr(x), xt, ld, _ptr(offs), _ptr(pos), T, offs.numel() - 1, k, H,
+                              _ptr(xs), _stream(x.device))
+    _raise("bgt_moe_gather", st)
+    return xs
+
+
+def moe_combine(ys, pos, weights=None, y=None):
+    """y[t] = sum_i weights[t][i] * ys[pos[t][i]] (weights None: all 1), T x H in
+    ys's dtype; places with pos -1 are skipped."""
+    torch = _torch()
+    _check(pos, "pos", torch.int32)
+    if pos.dim() != 2:
+        raise ValueError("pos must be T x k")
+    T, k = pos.shape
+    _check(ys, "ys", ys.dtype)
+    yt = _elem_type(ys, "ys")
+    if ys.dim() != 2 or ys.shape[0] != T * k:
+        raise ValueError("ys must be T*k x H")
+    H = ys.shape[1]
+    if weights is not None:
+        _check(weights, "weights", torch.float32, (T, k))
+    y = torch.empty((T, H), dtype=ys.dtype, device=ys.device) if y is None else y
+    _check(y, "y", ys.dtype, (T, H))
+    st = lib().bgt_moe_combine(_ptr(ys), yt, _ptr(pos), _ptr(weights), T, k, H, _ptr(y),
+                               _stream(ys.device))
+    _raise("bgt_moe_combine", st)
+    return y
+
+
+def moe_gather_backward(dxs, pos, dx=None):
+    """Gradient of moe_gather: dx[t] = sum_i dxs[pos[t][i]]."""
+    return moe_combine(dxs, pos, None, dx)
+
+
+def moe_combine_backward(dy, ys, offs, pos, weights, dys=None, dweights=None):
+    """Gradients of moe_combine for its rows (T*k x H, ys's dtype; zero past
+    offs[-1]) and its weights (T x k float32)."""
+    torch = _torch()
+    T, H, ld = _rows(dy, "dy")
+    yt = _elem_type(dy, "dy")
+    _check(offs, "offs", torch.int32)
+    _check(pos, "pos", torch.int32)
+    if pos.dim() != 2 or pos.shape[0] != T:
+        raise ValueError("pos must be T x k")
+    k = pos.shape[1]
+    _check(ys, "ys", dy.dtype, (T * k, H))
+    _check(weights, "weights", torch.float32, (T, k))
+    dys = torch.empty_like(ys) if dys is None else dys
+    if dweights is None:
+        dweights = torch.empty((T, k), dtype=torch.float32, device=dy.device)
+    _check(dys, "dys", dy.dtype, (T * k, H))
+    _check(dweights, "dweights", torch.float32, (T, k))
+    st = lib().bgt_moe_combine_backward(_ptr(dy), ld, _ptr(ys), yt, _ptr(offs), _ptr(pos),
+                                        _ptr(weights), T, offs.numel() - 1, k, H, _ptr(dys),
+                                        _ptr(dweights), _stream(dy.device))
+    _raise("bgt_moe_combine_backward", st)
+    return dys, dweights
+
+
+# ---------------------------------------------- weight-only products of few rows
+def w4a16_gemv(x, packed, fscale, N: int, y=None, out_dtype=None):
+    """x (M x K float32, float16 or bfloat16, not quantized) times the 4-bit
+    weights of pack_weights_int4 with their float scales ((K/128) x N); y in y's
+    dtype, else out_dtype, else x's. Meant for few rows."""
+    torch = _torch()
+    M, K, ld = _rows(x, "x")
+    xt = _elem_type(x, "x")
+    _check(packed, "packed", torch.uint8, (N * K // 2,))
+    _check(fscale, "fscale", torch.float32, (K // GROUP, N))
+    if y is None:
+        y = torch.empty((M, N), dtype=out_dtype or x.dtype, device=x.device)
+    _check(y, "y", y.dtype, (M, N))
+    st = lib().bgt_w4a16_gemv(_ptr(x), xt, ld, _ptr(packed), _ptr(fscale), M, N, K, _ptr(y),
+                              _elem_type(y, "y"), _stream(x.device))
+    _raise("bgt_w4a16_gemv", st)
+    return y
+
+
+def w4a16_moe_gemv(x, offsets, slot_token, packed, fscale, N: int, y=None, out_dtype=None):
+    """w4a16_gemv for routed slots: row r of y (R x N) is x[slot_token[r]] times
+    the weights of the expert whose offsets hold r; rows past offsets[-1] are
+    zero. packed (E x N*K/2 uint8), fscale (E x K/128 x N float32)."""
+    torch = _torch()
+    T, K, ld = _rows(x, "x")
+    xt = _elem_type(x, "x")
+    _check(offsets, "offsets", torch.int32)
+    _check(slot_token, "slot_token", torch.int32)
+    E, R = offsets.numel() - 1, slot_token.numel()
+    _check(packed, "packed", torch.uint8, (E, N * K // 2))
+    _check(fscale, "fscale", torch.float32, (E, K // GROUP, N))
+    if y is None:
+        y = torch.empty((R, N), dtype=out_dtype or x.dtype, device=x.device)
+    _check(y, "y", y.dtype, (R, N))
+    st = lib().bgt_w4a16_moe_gemv(_ptr(x), xt, ld, T, _ptr(offsets), _ptr(slot_token), E, R,
+                                  _ptr(packed), _ptr(fscale), N, K, _ptr(y), _elem_type(y, "y"),
+                                  _stream(x.device))
+    _raise("bgt_w4a16_moe_gemv", st)
+    return y

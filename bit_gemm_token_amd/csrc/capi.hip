@@ -342,4 +342,161 @@ int bgt_w8a8_gemm_zp(const uint8_t* qx, const float* sx, const int32_t* zx,
                                         acc_out, static_cast<hipStream_t>(stream)));
 }
 
+// ---------------------------------------------- mixture-of-experts routing
+namespace {
+
+// T tokens, E experts, k experts a token
+int check_route_shape(int64_t T, int64_t E, int64_t k) {
+  if (E < 1 || E > 256 || k < 1 || k > 16 || k > E) return BGT_ERR_SHAPE;
+  if (T < 1 || T > (1 << 24) / k) return BGT_ERR_SHAPE;
+  return BGT_OK;
+}
+
+bool aligned_to(const void* p, int bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) == 0;
+}
+int type_bytes(int t) { return t == BGT_F32 ? 4 : 2; }
+
+// the sort's workspace: ws may be NULL where none is needed
+int check_sort_ws(int64_t T, int64_t E, int64_t k, const void* ws, int64_t ws_bytes) {
+  const int64_t need = bgt::moe_sort_ws_bytes(T, E, k);
+  if (need == 0) return BGT_OK;
+  if (!ws) return BGT_ERR_NULL;
+  if (ws_bytes < need) return BGT_ERR_SHAPE;
+  return aligned_to(ws, 4) ? BGT_OK : BGT_ERR_ALIGN;
+}
+
+}  // namespace
+
+int64_t bgt_moe_sort_workspace_bytes(int64_t T, int64_t E, int64_t k) {
+  const int st = check_route_shape(T, E, k);
+  return st != BGT_OK ? st : bgt::moe_sort_ws_bytes(T, E, k);
+}
+
+int bgt_moe_route(const void* logits, int type, int64_t ld, int64_t T, int64_t E, int64_t k,
+                  int norm, float* weights, int32_t* ids, int32_t* offs, int32_t* tok,
+                  int32_t* pos, void* ws, int64_t ws_bytes, void* stream) {
+  if (!logits || !weights || !ids || !offs || !tok || !pos) return BGT_ERR_NULL;
+  if (!valid_type(type) || (norm != BGT_NORM_CHOSEN && norm != BGT_NORM_ALL)) return BGT_ERR_MODE;
+  int st = check_route_shape(T, E, k);
+  if (st != BGT_OK) return st;
+  if (ld < E) return BGT_ERR_SHAPE;
+  if (!aligned_to(logits, type_bytes(type)) || !aligned_to(weights, 4) || !aligned_to(ids, 4) ||
+      !aligned_to(offs, 4) || !aligned_to(tok, 4) || !aligned_to(pos, 4))
+    return BGT_ERR_ALIGN;
+  st = check_sort_ws(T, E, k, ws, ws_bytes);
+  if (st != BGT_OK) return st;
+  return hip_status(bgt::launch_moe_route(logits, type, ld, T, E, k, norm == BGT_NORM_ALL, weights,
+                                          ids, offs, tok, pos, static_cast<int32_t*>(ws),
+                                          static_cast<hipStream_t>(stream)));
+}
+
+int bgt_moe_sort(const int32_t* ids, int64_t T, int64_t E, int64_t k, int32_t* offs, int32_t* tok,
+                 int32_t* pos, void* ws, int64_t ws_bytes, void* stream) {
+  if (!ids || !offs || !tok || !pos) return BGT_ERR_NULL;
+  int st = check_route_shape(T, E, k);
+  if (st != BGT_OK) return st;
+  if (!aligned_to(ids, 4) || !aligned_to(offs, 4) || !aligned_to(tok, 4) || !aligned_to(pos, 4))
+    return BGT_ERR_ALIGN;
+  st = check_sort_ws(T, E, k, ws, ws_bytes);
+  if (st != BGT_OK) return st;
+  return hip_status(bgt::launch_moe_sort(ids, T, E, k, offs, tok, pos, static_cast<int32_t*>(ws),
+                                         static_cast<hipStream_t>(stream)));
+}
+
+int bgt_moe_route_backward(const float* dweights, const void* logits, int type, int64_t ld,
+                           const int32_t* ids, int64_t T, int64_t E, int64_t k, int norm,
+                           void* dlogits, void* stream) {
+  if (!dweights || !logits || !ids || !dlogits) return BGT_ERR_NULL;
+  if (!valid_type(type) || (norm != BGT_NORM_CHOSEN && norm != BGT_NORM_ALL)) return BGT_ERR_MODE;
+  const int st = check_route_shape(T, E, k);
+  if (st != BGT_OK) return st;
+  if (ld < E) return BGT_ERR_SHAPE;
+  if (!aligned_to(logits, type_bytes(type)) || !aligned_to(dlogits, type_bytes(type)) ||
+      !aligned_to(dweights, 4) || !aligned_to(ids, 4))
+    return BGT_ERR_ALIGN;
+  return hip_status(bgt::launch_moe_route_backward(dweights, logits, type, ld, ids, T, E, k,
+                                                   norm == BGT_NORM_ALL, dlogits,
+                                                   static_cast<hipStream_t>(stream)));
+}
+
+int bgt_moe_gather(const void* x, int type, int64_t ldx, const int32_t* offs, const int32_t* pos,
+                   int64_t T, int64_t E, int64_t k, int64_t H, void* xs, void* stream) {
+  if (!x || !offs || !pos || !xs) return BGT_ERR_NULL;
+  if (!valid_type(type)) return BGT_ERR_MODE;
+  const int st = check_route_shape(T, E, k);
+  if (st != BGT_OK) return st;
+  if (H < 1 || H > (1 << 20) || ldx < H) return BGT_ERR_SHAPE;
+  if (!aligned_to(x, type_bytes(type)) || !aligned_to(xs, type_bytes(type)) ||
+      !aligned_to(offs, 4) || !aligned_to(pos, 4))
+    return BGT_ERR_ALIGN;
+  return hip_status(bgt::launch_moe_gather(x, type, ldx, offs, pos, T, E, k, H, xs,
+                                           static_cast<hipStream_t>(stream)));
+}
+
+int bgt_moe_combine(const void* ys, int type, const int32_t* pos, const float* weights, int64_t T,
+                    int64_t k, int64_t H, void* y, void* stream) {
+  if (!ys || !pos || !y) return BGT_ERR_NULL;
+  if (!valid_type(type)) return BGT_ERR_MODE;
+  const int st = check_route_shape(T, 256, k);
+  if (st != BGT_OK) return st;
+  if (H < 1 || H > (1 << 20)) return BGT_ERR_SHAPE;
+  if (!aligned_to(ys, type_bytes(type)) || !aligned_to(y, type_bytes(type)) ||
+      !aligned_to(pos, 4) || !aligned_to(weights, 4))
+    return BGT_ERR_ALIGN;
+  return hip_status(bgt::launch_moe_combine(ys, type, pos, weights, T, k, H, y,
+                                            static_cast<hipStream_t>(stream)));
+}
+
+int bgt_moe_combine_backward(const void* dy, int64_t lddy, const void* ys, int type,
+                             const int32_t* offs, const int32_t* pos, const float* weights,
+                             int64_t T, int64_t E, int64_t k, int64_t H, void* dys,
+                             float* dweights, void* stream) {
+  if (!dy || !ys || !offs || !pos || !weights || !dys || !dweights) return BGT_ERR_NULL;
+  if (!valid_type(type)) return BGT_ERR_MODE;
+  const int st = check_route_shape(T, E, k);
+  if (st != BGT_OK) return st;
+  if (H < 1 || H > (1 << 20) || lddy < H) return BGT_ERR_SHAPE;
+  const int b = type_bytes(type);
+  if (!aligned_to(dy, b) || !aligned_to(ys, b) || !aligned_to(dys, b) || !aligned_to(offs, 4) ||
+      !aligned_to(pos, 4) || !aligned_to(weights, 4) || !aligned_to(dweights, 4))
+    return BGT_ERR_ALIGN;
+  return hip_status(bgt::launch_moe_combine_backward(dy, lddy, ys, type, offs, pos, weights, T, E,
+                                                     k, H, dys, dweights,
+                                                     static_cast<hipStream_t>(stream)));
+}
+
+int bgt_w4a16_gemv(const void* x, int x_type, int64_t ldx, const uint8_t* packed,
+                   const float* fscale, int64_t M, int64_t N, int64_t K, void* y, int y_type,
+                   void* stream) {
+  if (!x || !packed || !fscale || !y) return BGT_ERR_NULL;
+  if (!valid_type(x_type) || !valid_type(y_type)) return BGT_ERR_MODE;
+  const int st = check_gemm_shape(M, N, K, 65536);
+  if (st != BGT_OK) return st;
+  if (ldx < K) return BGT_ERR_SHAPE;
+  if (!aligned16(packed) || !aligned16(fscale) || !aligned_to(x, type_bytes(x_type)) ||
+      !aligned16(y))
+    return BGT_ERR_ALIGN;
+  return hip_status(bgt::launch_w4a16(x, x_type, ldx, packed, fscale, M, N, K,
+                                      bgt::OutY{y, y_type}, static_cast<hipStream_t>(stream)));
+}
+
+int bgt_w4a16_moe_gemv(const void* x, int x_type, int64_t ldx, int64_t T,
+                       const int32_t* expert_offsets, const int32_t* slot_token, int64_t E,
+                       int64_t R, const uint8_t* packed, const float* fscale, int64_t N, int64_t K,
+                       void* y, int y_type, void* stream) {
+  if (!x || !expert_offsets || !slot_token || !packed || !fscale || !y) return BGT_ERR_NULL;
+  if (!valid_type(x_type) || !valid_type(y_type)) return BGT_ERR_MODE;
+  const int st = check_gemm_shape(T, N, K, 65536);
+  if (st != BGT_OK) return st;
+  if (ldx < K) return BGT_ERR_SHAPE;
+  if (E < 1 || E > 256 || R < 1 || R > T * E || R > (1 << 24)) return BGT_ERR_SHAPE;
+  if (!aligned16(packed) || !aligned16(fscale) || !aligned_to(x, type_bytes(x_type)) ||
+      !aligned16(y) || !aligned_to(expert_offsets, 4) || !aligned_to(slot_token, 4))
+    return BGT_ERR_ALIGN;
+  return hip_status(bgt::launch_w4a16_moe(x, x_type, ldx, T, expert_offsets, slot_token, E, R,
+                                          packed, fscale, N, K, bgt::OutY{y, y_type},
+                                          static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -114,4 +114,33 @@ hipError_t launch_w8a8_zp(const uint8_t* qx, const float* sx, const int32_t* zx,
                           const int32_t* zw, const int32_t* colsum_w, int64_t M, int64_t N,
                           int64_t K, float* y, int32_t* acc_out, hipStream_t stream);
 
+// ---- mixture-of-experts routing and rows (moe_route.hip, moe_rows.hip); `type`
+// is the element type of logits or rows, ld their row stride in elements
+int64_t moe_sort_ws_bytes(int64_t T, int64_t E, int64_t k);
+hipError_t launch_moe_sort(const int32_t* ids, int64_t T, int64_t E, int64_t k, int32_t* offs,
+                           int32_t* tok, int32_t* pos, int32_t* ws, hipStream_t stream);
+hipError_t launch_moe_route(const void* logits, int type, int64_t ld, int64_t T, int64_t E,
+                            int64_t k, bool all, float* weights, int32_t* ids, int32_t* offs,
+                            int32_t* tok, int32_t* pos, int32_t* ws, hipStream_t stream);
+hipError_t launch_moe_route_backward(const float* dw, const void* logits, int type, int64_t ld,
+                                     const int32_t* ids, int64_t T, int64_t E, int64_t k, bool all,
+                                     void* dlogits, hipStream_t stream);
+hipError_t launch_moe_gather(const void* x, int type, int64_t ld, const int32_t* offs,
+                             const int32_t* pos, int64_t T, int64_t E, int64_t k, int64_t H,
+                             void* xs, hipStream_t stream);
+hipError_t launch_moe_combine(const void* ys, int type, const int32_t* pos, const float* weights,
+                              int64_t T, int64_t k, int64_t H, void* y, hipStream_t stream);
+hipError_t launch_moe_combine_backward(const void* dy, int64_t ld, const void* ys, int type,
+                                       const int32_t* offs, const int32_t* pos,
+                                       const float* weights, int64_t T, int64_t E, int64_t k,
+                                       int64_t H, void* dys, float* dweights, hipStream_t stream);
+
+// ---- unquantized activations times 4-bit weights with float scales (gemv_w4a16.hip)
+hipError_t launch_w4a16(const void* x, int x_type, int64_t ldx, const uint8_t* packed,
+                        const float* fscale, int64_t M, int64_t N, int64_t K, OutY y,
+                        hipStream_t stream);
+hipError_t launch_w4a16_moe(const void* x, int x_type, int64_t ldx, int64_t T, const int32_t* offs,
+                            const int32_t* tok, int64_t E, int64_t R, const uint8_t* packed,
+                            const float* fscale, int64_t N, int64_t K, OutY y, hipStream_t stream);
+
 }  // namespace bgt

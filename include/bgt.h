@@ -1,8 +1,10 @@
 /*
  * bgt.h -- C ABI of libbgt: the fine-grained W4A8 integer-scale linear layer
  * Y = X.W on AMD MI355X (gfx950), its two controls (float-scale W4A8,
- * zero-point W8A8), and two variants of the same epilogue: fine-grained W8A8
- * with integer scales and the grouped (mixture-of-experts) W4A8 GEMM.
+ * zero-point W8A8), two variants of the same epilogue: fine-grained W8A8
+ * with integer scales and the grouped (mixture-of-experts) W4A8 GEMM, and the
+ * mixture-of-experts layer around it: routing, rows to expert order and back,
+ * and weight-only products of few rows.
  *
  * Pages cited:
  *   [IS] "Integer Scale: A Free Lunch for Faster Fine-grained Quantization of
@@ -409,6 +411,121 @@ int bgt_w8a8_gemm_is(const int8_t* qx, const float* sx, const int8_t* qw, const 
 /* Diagnostics: name of the kernel bgt_w8a8_gemm_is launches for this shape. */
 const char* bgt_w8a8_is_kernel_name(int64_t M, int64_t N, int64_t K);
 
+/*
+ * Mixture-of-experts routing and rows, around the experts' products
+ * ([IS] 5.3 applies the scheme to Mixtral 8x7B, whose layers route each token
+ * to 2 of 8 experts): the router's choice and the sorted slot list that the
+ * grouped products take, token rows to expert order and back, and their
+ * gradients. T tokens, E experts, k experts for each token, R = T*k slots,
+ * rows of H elements. Common requirements: 1 <= E <= 256,
+ * 1 <= k <= min(E, 16), T >= 1, T*k <= 2^24, 1 <= H <= 2^20; every pointer
+ * aligned to its elements (16-byte aligned rows that are whole multiples of 16
+ * bytes are faster). Every result is a fixed order of operations: calls on
+ * equal inputs give equal bits.
+ *
+ * bgt_moe_route -- for each token the k largest of its E logits, equal logits
+ * taking the lower expert; with m the largest,
+ *     w_ti = exp(l_ti - m) / S,   S = the sum of exp(l - m) over the chosen
+ *     experts (BGT_NORM_CHOSEN) or over all E (BGT_NORM_ALL), in fp32;
+ * then the slots (t, i) sorted by expert as bgt_moe_sort does. Logits of -inf
+ * (masked) and NaN are never chosen: a token with fewer than k others gets
+ * expert -1 and weight 0 in its last places, and a token with none gets
+ * nothing else. Finite logits of any size are ordinary ones, the type's
+ * lowest value included. A logit of +inf makes the token's weights NaN, and
+ * so does a NaN among its logits under BGT_NORM_ALL, as the formula does.
+ *
+ *   logits   T x E of element type `type` (widened exactly), row stride ld >= E.
+ *   weights  T x k float32;  ids  T x k int32, largest logit first.
+ *   offs     E+1 int32: expert e's slots are offs[e] .. offs[e+1]-1; offs[E] is
+ *            the number of slots that have an expert.
+ *   tok      R int32: the token of each sorted slot, -1 from offs[E] on.
+ *   pos      T x k int32: the sorted slot of (t, i), -1 where ids is -1.
+ *   ws       scratch of bgt_moe_sort_workspace_bytes(T, E, k) bytes, caller-owned
+ *            (may be NULL where that is 0; too small: BGT_ERR_SHAPE), used
+ *            within the call only.
+ */
+#define BGT_NORM_CHOSEN 0
+#define BGT_NORM_ALL 1
+int bgt_moe_route(const void* logits, int type, int64_t ld, int64_t T, int64_t E, int64_t k,
+                  int norm, float* weights, int32_t* ids, int32_t* offs, int32_t* tok,
+                  int32_t* pos, void* ws, int64_t ws_bytes, void* stream);
+
+/* bgt_moe_sort -- the sorted slot list of experts chosen elsewhere: ids T x k
+ * int32, a value outside [0, E) drops the slot. Slots of one expert keep the
+ * order of (t, i). offs, tok, pos and ws as in bgt_moe_route. */
+int bgt_moe_sort(const int32_t* ids, int64_t T, int64_t E, int64_t k, int32_t* offs, int32_t* tok,
+                 int32_t* pos, void* ws, int64_t ws_bytes, void* stream);
+
+/* Bytes of scratch that bgt_moe_route and bgt_moe_sort take for these sizes
+ * (0: none). Negative: the status of an invalid shape. */
+int64_t bgt_moe_sort_workspace_bytes(int64_t T, int64_t E, int64_t k);
+
+/* bgt_moe_route_backward -- gradient of the logits from that of the weights:
+ *     dl_tj = p_tj (d_tj - sum_n p_tn d_tn),
+ * d_tj = dweights[t][i] for the expert j = ids[t][i] and 0 for the others, p
+ * the softmax over the chosen experts (0 elsewhere) or over all (norm as in
+ * the forward call). Places with ids outside [0, E) have no gradient; a token
+ * with nothing to normalise over gets zeros. dlogits: T x E of `type`, dense. */
+int bgt_moe_route_backward(const float* dweights, const void* logits, int type, int64_t ld,
+                           const int32_t* ids, int64_t T, int64_t E, int64_t k, int norm,
+                           void* dlogits, void* stream);
+
+/* bgt_moe_gather -- token rows in expert order: xs[pos[t][i]] = x[t] (copied
+ * bits), rows offs[E] .. R-1 zero. x: T rows of H elements of `type`, row
+ * stride ldx >= H; xs: R x H. pos and offs as bgt_moe_route leaves them: each
+ * slot below offs[E] belongs to one (t, i). Values of pos outside [0, R) are
+ * skipped and offs[E] is clamped to [0, R], so other lists cannot reach
+ * outside the buffers, but leave rows unspecified. */
+int bgt_moe_gather(const void* x, int type, int64_t ldx, const int32_t* offs, const int32_t* pos,
+                   int64_t T, int64_t E, int64_t k, int64_t H, void* xs, void* stream);
+
+/* bgt_moe_combine -- expert rows back to the tokens:
+ *     y[t] = sum_i weights[t][i] * ys[pos[t][i]]   (i ascending, fp32 multiply-adds,
+ * rounded once to `type`); places with pos outside [0, R) are skipped, so a
+ * token without experts gets zeros. weights NULL: all 1, which is the gradient
+ * of bgt_moe_gather. ys: R x H, y: T x H, both dense, of `type`. */
+int bgt_moe_combine(const void* ys, int type, const int32_t* pos, const float* weights, int64_t T,
+                    int64_t k, int64_t H, void* y, void* stream);
+
+/* bgt_moe_combine_backward -- gradients of bgt_moe_combine:
+ *     dys[pos[t][i]] = weights[t][i] * dy[t] (rounded to `type`), rows
+ *     offs[E] .. R-1 zero;   dweights[t][i] = sum_h dy[t][h] ys[pos[t][i]][h]
+ *     in fp32, 0 where pos is outside [0, R).
+ * dy: T rows of H elements, row stride lddy >= H; ys, dys: R x H. */
+int bgt_moe_combine_backward(const void* dy, int64_t lddy, const void* ys, int type,
+                             const int32_t* offs, const int32_t* pos, const float* weights,
+                             int64_t T, int64_t E, int64_t k, int64_t H, void* dys,
+                             float* dweights, void* stream);
+
+/*
+ * bgt_w4a16_gemv -- few rows of unquantized activations times 4-bit weights
+ * (weight-only quantization, [QB] §2.3.3: for small batches the group-wise
+ * scheme compresses only the weights and keeps FP16 inputs and outputs):
+ *     p_ilj = sum_{k in group l} x_ik q_kj,   y_ij = sum_l fscale[l][j] * p_ilj,
+ * every sum in fp32 (x and q are exact in the products), y rounded once.
+ *
+ *   x       M x K of element type x_type, row stride ldx >= K.
+ *   packed, fscale  as bgt_pack_weights_int4 writes them (codes -8..7 accepted),
+ *           16-byte aligned.
+ *   y       M x N of y_type, 16-byte aligned.
+ * Requirements: M, N, K as bgt_w4a8_gemm_is. Any M is computed; the kernel
+ * streams the weights once for up to 64 rows (21 of fp32) and again for each
+ * further block of rows, so for many rows the W4A8 GEMMs are the faster way.
+ */
+int bgt_w4a16_gemv(const void* x, int x_type, int64_t ldx, const uint8_t* packed,
+                   const float* fscale, int64_t M, int64_t N, int64_t K, void* y, int y_type,
+                   void* stream);
+
+/* bgt_w4a16_moe_gemv -- the same for routed slots: y[r] = x[slot_token[r]]
+ * times expert e's weights, for offsets and slots as in bgt_w4a8_moe_gemm_is
+ * or bgt_moe_route; experts without slots read no weights. Rows
+ * expert_offsets[E] .. R-1 of y are zero. packed: E x (N*K/2) bytes, fscale:
+ * E x (K/128) x N. Requirements and clamping as bgt_w4a8_moe_gemm_is. */
+int bgt_w4a16_moe_gemv(const void* x, int x_type, int64_t ldx, int64_t T,
+                       const int32_t* expert_offsets, const int32_t* slot_token, int64_t E,
+                       int64_t R, const uint8_t* packed, const float* fscale, int64_t N, int64_t K,
+                       void* y, int y_type, void* stream);
+
 /* Human-readable text of a status code (static storage). */
 const char* bgt_status_string(int status);
 
@@ -418,7 +535,9 @@ const char* bgt_status_string(int status);
  * 105 the grouped (mixture-of-experts) W4A8 integer-scale GEMM, 106 the
  * expert count and slot count in bgt_w4a8_moe_kernel_name, 107 the canonical
  * int4 layout (bgt_repack_int4_canonical), 108 bgt_set_prefill_kernel and
- * bgt_w4a8_workspace_bytes, 109 bgt_w4a8_gemm_is_noalloc. */
+ * bgt_w4a8_workspace_bytes, 109 bgt_w4a8_gemm_is_noalloc. The bgt_moe_* and
+ * bgt_w4a16_* entry points came after 109 as symbols of their own, with no
+ * change to what 109 names, and are found by their symbols. */
 int bgt_abi_version(void);
 
 /* Diagnostics: name of the GEMM kernel that bgt_w4a8_gemm_is (float_scale = 0)
