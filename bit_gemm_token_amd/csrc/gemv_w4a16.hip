@@ -29,7 +29,19 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 // loads of x at the alignment of its elements (one wide load all the same)
 typedef uint32_t u4e __attribute__((ext_vector_type(4), aligned(2)));
-typedef float f4e __attribute__((ext_vector_type(4), aligned(4)));
+typedef float f2e __attribute__((ext_vector_type(2), aligned(4)));
+
+// words of a wave's LDS block, written and read as different types
+typedef uint32_t u1a __attribute__((may_alias));
+typedef uint32_t u4a __attribute__((ext_vector_type(4), may_alias));
+
+// orders the wave's own LDS accesses (they execute in program order; this keeps
+// the compiler from moving them across)
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 
 // terms a row of x takes in A
 template <int XT> constexpr int kTerms = XT == kF32 ? 3 : 1;
@@ -37,73 +49,52 @@ template <int XT> constexpr int kTerms = XT == kF32 ? 3 : 1;
 __device__ __forceinline__ uint32_t perm(uint32_t hi, uint32_t lo, uint32_t sel) {
   return __builtin_amdgcn_perm(hi, lo, sel);
 }
-
-// The A operand of one MFMA: 8 consecutive elements of a row. fp16 elements are
-// reordered to (0,2 1,3 4,6 5,7), the order in which unpack_f16 leaves codes.
-template <int XT>
-__device__ __forceinline__ uint4 load_a(const void* row, int k, int term) {
-  if constexpr (XT == kF16) {
-    const u4e d = *reinterpret_cast<const u4e*>(static_cast<const uint16_t*>(row) + k);
-    return make_uint4(perm(d.y, d.x, 0x05040100u), perm(d.y, d.x, 0x07060302u),
-                      perm(d.w, d.z, 0x05040100u), perm(d.w, d.z, 0x07060302u));
-  } else if constexpr (XT == kBF16) {
-    const u4e d = *reinterpret_cast<const u4e*>(static_cast<const uint16_t*>(row) + k);
-    return make_uint4(d.x, d.y, d.z, d.w);
-  } else {
-    const f4e* p = reinterpret_cast<const f4e*>(static_cast<const float*>(row) + k);
-    const f4e a = p[0], b = p[1];
-    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    uint32_t t[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      // v = hi + mid + lo by truncation, each exact in bf16; infinities and
-      // NaN stay whole in the first term
-      const uint32_t u = __float_as_uint(v[i]);
-      const bool fin = (u & 0x7F800000u) != 0x7F800000u;
-      const float hi = __uint_as_float(u & 0xFFFF0000u);
-      const float r1 = v[i] - hi;
-      const float mid = __uint_as_float(__float_as_uint(r1) & 0xFFFF0000u);
-      const float lo = r1 - mid;
-      const uint32_t top = fin ? u : ((u & 0x007FFFFFu) ? 0x7FC00000u : u);
-      t[i] = term == 0 ? top : (!fin ? 0u : __float_as_uint(term == 1 ? mid : lo));
-    }
-    return make_uint4(perm(t[1], t[0], 0x07060302u), perm(t[3], t[2], 0x07060302u),
-                      perm(t[5], t[4], 0x07060302u), perm(t[7], t[6], 0x07060302u));
-  }
+__device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t mask, uint32_t flip) {
+  return (w & mask) ^ flip;
+}
+// upper halves of two words
+__device__ __forceinline__ uint32_t pack_hi(uint32_t hi, uint32_t lo) {
+  return perm(hi, lo, 0x07060302u);
 }
 
-// 8 codes of a packed word as the B operand. fp16: (1024 + n) - 1032 with
-// n = q + 8 set in the mantissa (or 1024 + 16n, times 1/16): exact. bf16: 16 q
-// by signed byte conversions, the upper halves packed; scaled back with the
-// group's scale (1/16, exact).
+// q / 16 in fp32 of the 4-bit two's complement q in the low nibble of byte B
+template <int B>
+__device__ __forceinline__ uint32_t sixteenth(uint32_t w) {
+  uint32_t f;
+  if constexpr (B == 0) asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_0" : "=v"(f) : "v"(w));
+  if constexpr (B == 1) asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_1" : "=v"(f) : "v"(w));
+  if constexpr (B == 2) asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_2" : "=v"(f) : "v"(w));
+  if constexpr (B == 3) asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_3" : "=v"(f) : "v"(w));
+  return f;
+}
+
+// 8 codes of a packed word as the B operand, k ascending. fp16: the nibbles of
+// bytes (0,1) and (2,3) in the mantissas of 1024 + n and 1024 + 16 n, n = q + 8
+// (sign bit flipped), less 1032, or times 1/16 less 72: exact. bf16: q / 16 in
+// fp32 from the low nibble of each byte, the upper halves packed; scaled back
+// with the group's scale (16, exact).
 template <int XT>
 __device__ __forceinline__ uint4 unpack(uint32_t w) {
   if constexpr (XT == kF16) {
-    const uint32_t n = w ^ 0x88888888u, n8 = n >> 8;
     const half2v lo = {(_Float16)-1032.0f, (_Float16)-1032.0f};
     const half2v sc = {(_Float16)0.0625f, (_Float16)0.0625f};
     const half2v hi = {(_Float16)-72.0f, (_Float16)-72.0f};
-    const uint32_t a = (n & 0x000F000Fu) | 0x64006400u, b = (n8 & 0x000F000Fu) | 0x64006400u;
-    const uint32_t c = (n & 0x00F000F0u) | 0x64006400u, d = (n8 & 0x00F000F0u) | 0x64006400u;
-    const half2v ah = __builtin_bit_cast(half2v, a) + lo, bh = __builtin_bit_cast(half2v, b) + lo;
-    const half2v ch = __builtin_elementwise_fma(__builtin_bit_cast(half2v, c), sc, hi);
-    const half2v dh = __builtin_elementwise_fma(__builtin_bit_cast(half2v, d), sc, hi);
-    return make_uint4(__builtin_bit_cast(uint32_t, ah), __builtin_bit_cast(uint32_t, bh),
-                      __builtin_bit_cast(uint32_t, ch), __builtin_bit_cast(uint32_t, dh));
+    const uint32_t u = perm(w, w, 0x01010000u), v = perm(w, w, 0x03030202u);
+    const half2v a = __builtin_bit_cast(half2v, and_xor(u, 0x000F000Fu, 0x64086408u)) + lo;
+    const half2v b = __builtin_bit_cast(half2v, and_xor(v, 0x000F000Fu, 0x64086408u)) + lo;
+    const half2v c = __builtin_elementwise_fma(
+        __builtin_bit_cast(half2v, and_xor(u, 0x00F000F0u, 0x64806480u)), sc, hi);
+    const half2v d = __builtin_elementwise_fma(
+        __builtin_bit_cast(half2v, and_xor(v, 0x00F000F0u, 0x64806480u)), sc, hi);
+    return make_uint4(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b),
+                      __builtin_bit_cast(uint32_t, c), __builtin_bit_cast(uint32_t, d));
   } else {
-    uint32_t lo, hi;
-    unpack_x16(w, lo, hi);
-    uint32_t f[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[i] = __float_as_uint((float)(int8_t)(lo >> (8 * i)));
-      f[4 + i] = __float_as_uint((float)(int8_t)(hi >> (8 * i)));
-    }
-    return make_uint4(perm(f[1], f[0], 0x07060302u), perm(f[3], f[2], 0x07060302u),
-                      perm(f[5], f[4], 0x07060302u), perm(f[7], f[6], 0x07060302u));
+    const uint32_t h = w >> 4;
+    return make_uint4(pack_hi(sixteenth<1>(w), sixteenth<0>(w)), pack_hi(sixteenth<3>(w), sixteenth<2>(w)),
+                      pack_hi(sixteenth<1>(h), sixteenth<0>(h)), pack_hi(sixteenth<3>(h), sixteenth<2>(h)));
   }
 }
-template <int XT> constexpr float kCodeScale = XT == kF16 ? 1.0f : 0.0625f;
+template <int XT> constexpr float kCodeScale = XT == kF16 ? 1.0f : 16.0f;
 
 template <int XT>
 __device__ __forceinline__ v4f mfma(const uint4& a, const uint4& b, v4f c) {
@@ -115,128 +106,382 @@ __device__ __forceinline__ v4f mfma(const uint4& a, const uint4& b, v4f c) {
                                                    __builtin_bit_cast(bfloat8, b), c, 0, 0, 0);
 }
 
-// One workgroup: NT column tiles of 16 for up to 16*MR / terms rows; its NW
-// waves split the groups, and their partial outputs are added in wave order.
-template <int XT, int MR, int NT, int NW, bool GR>
-__global__ __launch_bounds__(NW * 64) void k_w4a16(const void* __restrict__ x, int64_t ldx,
-                                                   const uint4* __restrict__ packed,
-                                                   const float* __restrict__ fscale, int M, int N,
-                                                   int G, OutY y, Route rt) {
-  constexpr int TERMS = kTerms<XT>, ROWS = 16 * MR / TERMS;
-  __shared__ float part[NW][MR][16][16 * NT];
-  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-  const int c = lane % 16, s4 = lane / 16;
-  const int t0 = blockIdx.x * NT, tiles = N / 16;
-  int first = 0, rows = M;
-  if constexpr (GR) {
-    const int e = blockIdx.y;
-    const int last = clamp_route(rt.offs[rt.E], 0, rt.R);
-    if (e == rt.E) {                               // rows past the last slot are zero
-      const int cols = min(16 * NT, N - 16 * t0);
-      for (int r = last; r < rt.R; ++r)
-        for (int j = threadIdx.x; j < cols; j += NW * 64) y.put((int64_t)r * N + 16 * t0 + j, 0.0f);
-      return;
-    }
-    first = clamp_route(rt.offs[e], 0, rt.R);
-    rows = clamp_route(rt.offs[e + 1], first, rt.R) - first;
-    packed += (int64_t)e * rt.wstride / 16;
-    fscale += (int64_t)e * rt.sstride;
-  }
-  const int gb = G * wave / NW, ge = G * (wave + 1) / NW;
-  for (int pass = blockIdx.z; pass * ROWS < rows; pass += gridDim.z) {
-    const int r0 = pass * ROWS, nr = min(ROWS, rows - r0);
-    const char* arow[MR];
-#pragma unroll
-    for (int rb = 0; rb < MR; ++rb) {
-      int i = first + r0 + min((rb * 16 + c) / TERMS, nr - 1);
-      if constexpr (GR) i = clamp_route(rt.tok[i], 0, rt.T - 1);
-      arow[rb] = static_cast<const char*>(x) + (int64_t)i * ldx * (XT == kF32 ? 4 : 2);
-    }
-    v4f acc[MR][NT];
-#pragma unroll
-    for (int rb = 0; rb < MR; ++rb)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) acc[rb][nt] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+// ---------------------------------------------------------- rows of x as A
+// The wave reads a group of each row in whole 256-byte runs and turns it into
+// operands through an LDS block of its own (256 bytes a row; 16-byte pieces
+// exchanged by row so that the 16 rows of an operand read fall on distinct
+// banks). Loading operands directly, 16 bytes from each of 16 rows, takes the
+// address path a request for every lane. No other wave touches the block.
+// QR: rows in use, in fours (those past the last repeat it; the block's rows
+// past 4*QR are never written, and nobody reads the outputs of either).
+__device__ __forceinline__ uint4 lds_operand(const char* lds, int rb, int m) {
+  const int lane = threadIdx.x % kWave, c = lane % 16;
+  const int piece = 8 * (m / 2) + 2 * (lane / 16) + m % 2;
+  const u4a v = *reinterpret_cast<const u4a*>(lds + (16 * rb + c) * 256 + (piece ^ c) * 16);
+  return make_uint4(v.x, v.y, v.z, v.w);
+}
 
-    for (int g = gb; g < ge; ++g) {
-      uint4 a[MR][4];
+// fp16 / bf16: 16 lanes a row
+template <int XT, int QR>
+struct Rows {
+  const uint16_t* x;             // at the lane's piece
+  int64_t ldx;
+  int row[QR];                   // row 4i + lane/16 of this pass, as a row of x
+  char* lds;
+  // slot(i): row index in x of row i of this pass (i < nr)
+  template <typename F>
+  __device__ __forceinline__ Rows(const void* xp, int64_t ld, int nr, char* block, F slot)
+      : x(static_cast<const uint16_t*>(xp) + 8 * (threadIdx.x % 16)), ldx(ld), lds(block) {
 #pragma unroll
-      for (int rb = 0; rb < MR; ++rb)
+    for (int i = 0; i < QR; ++i)
+      row[i] = slot(min(4 * i + (int)(threadIdx.x % kWave) / 16, nr - 1));
+  }
+  struct Raw { u4e v[QR]; };
+  __device__ __forceinline__ void load(Raw& r, int g) const {
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
-          a[rb][m] = load_a<XT>(arow[rb], g * kGroup + 64 * (m / 2) + 16 * s4 + 8 * (m % 2),
-                                (rb * 16 + c) % TERMS);
+    for (int i = 0; i < QR; ++i)
+      r.v[i] = *reinterpret_cast<const u4e*>(x + row[i] * ldx + (int64_t)g * kGroup);
+  }
+  __device__ __forceinline__ void stage(const Raw& r) const {
+    const int lane = threadIdx.x % kWave;
+    wave_fence();                                  // the last group's reads come first
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int t = min(t0 + nt, tiles - 1);
-        const uint4 w = load_u4_nt(packed + ((int64_t)t * G + g) * 64 + lane);
-        const float sc = fscale[(int64_t)g * N + 16 * t + c] * kCodeScale<XT>;
-        const uint4 b0 = unpack<XT>(w.x), b1 = unpack<XT>(w.y), b2 = unpack<XT>(w.z),
-                    b3 = unpack<XT>(w.w);
+    for (int i = 0; i < QR; ++i) {
+      const int vr = 4 * i + lane / 16;
+      *reinterpret_cast<u4a*>(lds + vr * 256 + ((lane % 16) ^ (vr % 16)) * 16) = r.v[i];
+    }
+    wave_fence();
+  }
+};
+
+// fp32: 2 elements a lane; every element is split once, row i into rows 3i..3i+2
+template <int QR>
+struct Rows<kF32, QR> {
+  static constexpr int ROWS = 4 * QR / 3;
+  const float* x;
+  int64_t off[ROWS];
+  int nr;
+  char* lds;
+  template <typename F>
+  __device__ __forceinline__ Rows(const void* xp, int64_t ldx, int rows, char* block, F slot)
+      : x(static_cast<const float*>(xp)), nr(rows), lds(block) {
 #pragma unroll
-        for (int rb = 0; rb < MR; ++rb) {
-          v4f p = {0.0f, 0.0f, 0.0f, 0.0f};
-          p = mfma<XT>(a[rb][0], b0, p);
-          p = mfma<XT>(a[rb][1], b1, p);
-          p = mfma<XT>(a[rb][2], b2, p);
-          p = mfma<XT>(a[rb][3], b3, p);
+    for (int i = 0; i < ROWS; ++i)
+      off[i] = (int64_t)__builtin_amdgcn_readfirstlane(slot(min(i, nr - 1))) * ldx;
+  }
+  struct Raw { f2e v[ROWS]; };
+  __device__ __forceinline__ void load(Raw& r, int g) const {
+    const int lane = threadIdx.x % kWave;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[rb][nt][r] = fmaf(p[r], sc, acc[rb][nt][r]);
+    for (int i = 0; i < ROWS; ++i)
+      r.v[i] = *reinterpret_cast<const f2e*>(x + off[i] + (int64_t)g * kGroup + 2 * lane);
+  }
+  // v = hi + mid + lo by truncation, each exact in bf16 (its upper half); an
+  // infinity or NaN stays whole in the first term (made quiet, so that its upper
+  // half is a NaN too)
+  __device__ __forceinline__ static void split(float v, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+    v = __builtin_canonicalizef(v);
+    hi = __float_as_uint(v);
+    const float r1 = __builtin_isfinite(v) ? v - __uint_as_float(hi & 0xFFFF0000u) : 0.0f;
+    mid = __float_as_uint(r1);
+    lo = __float_as_uint(r1 - __uint_as_float(mid & 0xFFFF0000u));
+  }
+  __device__ __forceinline__ void stage(const Raw& r) const {
+    const int lane = threadIdx.x % kWave;
+    wave_fence();                                  // the last group's reads come first
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      if (i < nr) {
+        uint32_t t0[3], t1[3];
+        split(r.v[i].x, t0[0], t0[1], t0[2]);
+        split(r.v[i].y, t1[0], t1[1], t1[2]);
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+          const int vr = 3 * i + q;
+          *reinterpret_cast<u1a*>(lds + vr * 256 + ((lane / 4) ^ (vr % 16)) * 16 + (lane % 4) * 4) =
+              pack_hi(t1[q], t0[q]);
         }
       }
     }
+    wave_fence();
+  }
+};
+
+// ------------------------------------------------------------------- kernel
+template <int QR> constexpr int kBlocks = (QR + 3) / 4;      // row blocks of 16
+
+// The wave's groups [gb, ge) of NT column tiles, D groups in flight.
+// make_rows() is called once the first weights have been requested (the row
+// list of routed slots is itself loaded).
+template <int XT, int QR, int NT, int D, typename F>
+__device__ __forceinline__ void run_groups(F make_rows, const uint4* __restrict__ packed,
+                                           const float* __restrict__ fscale, int t0, int tiles,
+                                           int N, int G, int gb, int ge,
+                                           v4f (&acc)[kBlocks<QR>][NT]) {
+  constexpr int MR = kBlocks<QR>;
+  const int lane = threadIdx.x % kWave, c = lane % 16;
+  // wave-uniform bases, the lane's part added by each load
+  const uint4* wp[NT];
+  const float* sp[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int t = min(t0 + nt, tiles - 1);         // a tile past the last repeats it, unused
+    wp[nt] = packed + (int64_t)t * G * 64;
+    sp[nt] = fscale + 16 * t;
+  }
+  typename Rows<XT, QR>::Raw a[D];
+  uint4 w[D][NT];
+  float s[D][NT];
+  auto load = [&](int u, int g) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const uint4* p = wp[nt] + (int64_t)g * 64 + lane;
+      w[u][nt] = *p;
+      s[u][nt] = (sp[nt] + (int64_t)g * N)[c];
+    }
+  };
+  if (gb >= ge) return;
+#pragma unroll
+  for (int u = 0; u < D; ++u) load(u, min(gb + u, ge - 1));
+  const Rows<XT, QR> rows = make_rows();
+#pragma unroll
+  for (int u = 0; u < D; ++u) rows.load(a[u], min(gb + u, ge - 1));
+  auto compute = [&](int u) {
+    rows.stage(a[u]);
+    uint4 op[MR][4];
 #pragma unroll
     for (int rb = 0; rb < MR; ++rb)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int m = 0; m < 4; ++m) op[rb][m] = lds_operand(rows.lds, rb, m);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) part[wave][rb][4 * s4 + r][16 * nt + c] = acc[rb][nt][r];
-    __syncthreads();
-    for (int o = threadIdx.x; o < nr * 16 * NT; o += NW * 64) {
-      const int i = o / (16 * NT), j = o % (16 * NT);
-      if (16 * t0 + j < N) {
-        float v = 0.0f;
+    for (int nt = 0; nt < NT; ++nt) {
+      const uint4 b0 = unpack<XT>(w[u][nt].x), b1 = unpack<XT>(w[u][nt].y),
+                  b2 = unpack<XT>(w[u][nt].z), b3 = unpack<XT>(w[u][nt].w);
+      const float sc = s[u][nt] * kCodeScale<XT>;
 #pragma unroll
-        for (int w = 0; w < NW; ++w)
+      for (int rb = 0; rb < MR; ++rb) {
+        v4f p = {0.0f, 0.0f, 0.0f, 0.0f};
+        p = mfma<XT>(op[rb][0], b0, p);
+        p = mfma<XT>(op[rb][1], b1, p);
+        p = mfma<XT>(op[rb][2], b2, p);
+        p = mfma<XT>(op[rb][3], b3, p);
 #pragma unroll
-          for (int q = TERMS - 1; q >= 0; --q) {
-            const int vr = i * TERMS + q;
-            v += part[w][vr / 16][vr % 16][j];
-          }
-        y.put((int64_t)(first + r0 + i) * N + 16 * t0 + j, v);
+        for (int r = 0; r < 4; ++r) acc[rb][nt][r] = __builtin_fmaf(p[r], sc, acc[rb][nt][r]);
       }
     }
-    __syncthreads();
+  };
+  int g = gb;
+  for (; g + D < ge; g += D) {
+#pragma unroll
+    for (int u = 0; u < D; ++u) {
+      compute(u);
+      const int next = min(g + D + u, ge - 1);
+      load(u, next);
+      rows.load(a[u], next);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < D; ++u)
+    if (g + u < ge) compute(u);
+}
+
+// One workgroup: NT column tiles of 16 for up to 4*QR / terms rows; its NW
+// waves split the groups, and their partial outputs are added in wave order.
+template <int XT, int QR, int NT, int NW, int D>
+__device__ __forceinline__ void run_rows(char* lds, const void* x, int64_t ldx, const uint4* packed,
+                                         const float* fscale, int N, int G, OutY y, const Route& rt,
+                                         bool routed, int first, int nr) {
+  constexpr int TERMS = kTerms<XT>, MR = kBlocks<QR>;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  const int c = lane % 16, s4 = lane / 16;
+  const int t0 = blockIdx.x * NT;
+  auto make_rows = [&] {
+    return Rows<XT, QR>(x, ldx, nr, lds + wave * MR * 4096, [&](int i) {
+      return routed ? clamp_route(rt.tok[first + i], 0, rt.T - 1) : first + i;
+    });
+  };
+  v4f acc[MR][NT];
+#pragma unroll
+  for (int rb = 0; rb < MR; ++rb)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) acc[rb][nt] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  run_groups<XT, QR, NT, D>(make_rows, packed, fscale, t0, N / 16, N, G, G * wave / NW,
+                            G * (wave + 1) / NW, acc);
+  float* part = reinterpret_cast<float*>(lds);     // [NW][16 MR][16 NT]
+  __syncthreads();                                 // the waves' row blocks are done with
+#pragma unroll
+  for (int rb = 0; rb < MR; ++rb)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        part[((wave * MR + rb) * 16 + 4 * s4 + r) * (16 * NT) + 16 * nt + c] = acc[rb][nt][r];
+  __syncthreads();
+  for (int o = threadIdx.x; o < nr * 16 * NT; o += NW * 64) {
+    const int i = o / (16 * NT), j = o % (16 * NT);
+    if (16 * t0 + j < N) {
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w)
+#pragma unroll
+        for (int q = TERMS - 1; q >= 0; --q) v += part[(w * 16 * MR + i * TERMS + q) * (16 * NT) + j];
+      y.put((int64_t)(first + i) * N + 16 * t0 + j, v);
+    }
+  }
+  __syncthreads();
+}
+
+template <int QR, int NT, int NW>
+constexpr int kLds = (NT < 4 ? 4 : NT) * 1024 * NW * kBlocks<QR>;
+
+// dense: up to 4*QR / terms rows a pass, grid z over the passes
+template <int XT, int QR, int NT, int NW, int D>
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) void k_w4a16(
+    const void* __restrict__ x, int64_t ldx, const uint4* __restrict__ packed,
+    const float* __restrict__ fscale, int M, int N, int G, OutY y) {
+  __shared__ __attribute__((aligned(16))) char lds[kLds<QR, NT, NW>];
+  constexpr int ROWS = 4 * QR / kTerms<XT>;
+  const int r0 = blockIdx.z * ROWS;
+  run_rows<XT, QR, NT, NW, D>(lds, x, ldx, packed, fscale, N, G, y, Route{}, false, r0,
+                              min(ROWS, M - r0));
+}
+
+// The j-th expert that has slots: its number, first slot and slot count. Every
+// wave reads the offsets 64 experts at a time. False: fewer experts have slots.
+__device__ __forceinline__ bool busy_expert(const Route& rt, int j, int& e, int& first, int& rows) {
+  const int lane = threadIdx.x % kWave;
+  for (int base = 0; base < rt.E; base += kWave) {
+    const int i = min(base + lane, rt.E - 1);
+    const int a = clamp_route(rt.offs[i], 0, rt.R), b = clamp_route(rt.offs[i + 1], a, rt.R);
+    const unsigned long long busy = __ballot(base + lane < rt.E && b > a);
+    const int n = __popcll(busy);
+    if (j < n) {
+      const unsigned long long mine = __ballot(__popcll(busy & ((2ull << lane) - 1)) == j + 1) & busy;
+      const int l = __builtin_ctzll(mine);
+      e = __builtin_amdgcn_readfirstlane(base + l);
+      first = __builtin_amdgcn_readfirstlane(__shfl(a, l, kWave));
+      rows = __builtin_amdgcn_readfirstlane(__shfl(b, l, kWave)) - first;
+      return true;
+    }
+    j -= n;
+  }
+  return false;
+}
+
+// routed: grid y counts the experts that have slots (at most one a slot, so the
+// grid of a few slots has few rows); an expert's slots go through in passes of
+// up to 4*QR / terms rows (16 of A where that is enough). The first y zeroes
+// the rows past the last slot.
+template <int XT, int QR, int NT, int NW, int D>
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) void k_w4a16_moe(
+    const void* __restrict__ x, int64_t ldx, const uint4* __restrict__ packed,
+    const float* __restrict__ fscale, int N, int G, OutY y, Route rt) {
+  __shared__ __attribute__((aligned(16))) char lds[kLds<QR, NT, NW>];
+  constexpr int TERMS = kTerms<XT>;
+  if (blockIdx.y == 0) {
+    const int c0 = 16 * NT * blockIdx.x, cols = min(16 * NT, N - c0);
+    for (int r = clamp_route(rt.offs[rt.E], 0, rt.R); r < rt.R; ++r)
+      for (int j = threadIdx.x; j < cols; j += NW * 64) y.put((int64_t)r * N + c0 + j, 0.0f);
+  }
+  int e, first, rows;
+  if (!busy_expert(rt, blockIdx.y, e, first, rows)) return;
+  packed += (int64_t)e * rt.wstride / 16;
+  fscale += (int64_t)e * rt.sstride;
+  for (int r0 = 0, nr = 0; r0 < rows; r0 += nr) {
+    nr = min(rows - r0, 4 * QR / TERMS);
+    if (QR > 4 && nr * TERMS <= 16)
+      run_rows<XT, 4, NT, NW, D>(lds, x, ldx, packed, fscale, N, G, y, rt, true, first + r0, nr);
+    else
+      run_rows<XT, QR, NT, NW, D>(lds, x, ldx, packed, fscale, N, G, y, rt, true, first + r0, nr);
   }
 }
 
-template <int XT, int MR, bool GR>
-static void launch_mr(const void* x, int64_t ldx, const uint8_t* packed, const float* fscale, int M,
-                      int N, int K, OutY y, const Route& rt, hipStream_t stream) {
-  constexpr int ROWS = 16 * MR / kTerms<XT>;
+template <int XT, int QR, int NT, int NW, int D>
+static void launch_dense(const void* x, int64_t ldx, const uint8_t* packed, const float* fscale,
+                         int M, int N, int K, OutY y, hipStream_t stream) {
+  constexpr int ROWS = 4 * QR / kTerms<XT>;
   const int tiles = N / 16;
-  const dim3 grid(tiles, GR ? rt.E + 1 : 1, GR ? 1 : (M + ROWS - 1) / ROWS);
-  hipLaunchKernelGGL((k_w4a16<XT, MR, 1, 8, GR>), grid, dim3(512), 0, stream, x, ldx,
-                     reinterpret_cast<const uint4*>(packed), fscale, M, N, K / kGroup, y, rt);
+  const dim3 grid((tiles + NT - 1) / NT, 1, (M + ROWS - 1) / ROWS);
+  hipLaunchKernelGGL((k_w4a16<XT, QR, NT, NW, D>), grid, dim3(NW * 64), 0, stream, x, ldx,
+                     reinterpret_cast<const uint4*>(packed), fscale, M, N, K / kGroup, y);
+}
+template <int XT, int QR, int NT, int NW, int D>
+static void launch_routed(const void* x, int64_t ldx, const uint8_t* packed, const float* fscale,
+                          int N, int K, OutY y, const Route& rt, hipStream_t stream) {
+  const int tiles = N / 16;
+  hipLaunchKernelGGL((k_w4a16_moe<XT, QR, NT, NW, D>), dim3((tiles + NT - 1) / NT, min(rt.E, rt.R)),
+                     dim3(NW * 64), 0, stream, x, ldx, reinterpret_cast<const uint4*>(packed),
+                     fscale, N, K / kGroup, y, rt);
+}
+#ifndef BGT_GEMV_SWEEP
+// Column tiles a workgroup takes, for `tiles` tiles in the whole launch and QR
+// row quads: what the busiest CU then has to do, each workgroup's rows counted
+// as 0.3 tiles a quad. Sweeps (us), 2 / 3 / 4 tiles a workgroup: 16 x 4096 x
+// 22016 fp16 (1376 tiles) 13.9 / 11.9 / 14.9; 8 experts of 14336 x 4096, 61
+// tokens fp16 (2048 tiles) 71.5 / 69.1 / 55.0; 2 of 4096 x 14336, 1 token bf16
+// (1792 tiles) 15.1 / 17.6 / 14.4. Up to one tile a CU: 1 (1 x 4096 x 4096:
+// 3.5, with 2 tiles 5.1).
+static int tiles_per_wg(int tiles, int qr) {
+  const int cus = device_cus();
+  if (tiles <= cus) return 1;
+  int best = 2;
+  float least = 0.0f;
+  for (int nt = 2; nt <= 4; ++nt) {
+    const int wgs = (tiles + nt - 1) / nt;
+    const float cost = (float)((wgs + cus - 1) / cus) * ((float)nt + 0.3f * (float)qr);
+    if (nt == 2 || cost <= least) { best = nt; least = cost; }
+  }
+  return best;
 }
 
-template <int XT, bool GR>
-static void launch_type(const void* x, int64_t ldx, const uint8_t* packed, const float* fscale,
-                        int M, int N, int K, OutY y, const Route& rt, hipStream_t stream) {
-  const int blocks = (M * kTerms<XT> + 15) / 16;   // row blocks of A
-  if (blocks <= 1) launch_mr<XT, 1, GR>(x, ldx, packed, fscale, M, N, K, y, rt, stream);
-  else if (blocks == 2) launch_mr<XT, 2, GR>(x, ldx, packed, fscale, M, N, K, y, rt, stream);
-  else launch_mr<XT, 4, GR>(x, ldx, packed, fscale, M, N, K, y, rt, stream);
+// f(QR, NT, NW, D) for rows of A and the tile count. One tile a workgroup gets
+// 8 waves, since there is then one workgroup a CU or fewer; two or more get 4.
+template <typename F>
+static void with_shape(int rows, int tiles, F f) {
+  const auto by_tiles = [&](auto qr) {
+    constexpr int QR = decltype(qr)::value;
+    switch (tiles_per_wg(tiles, QR)) {
+      case 1: f(qr, IC<1>{}, IC<8>{}, IC<QR <= 4 ? 2 : 1>{}); break;
+      case 2: f(qr, IC<2>{}, IC<4>{}, IC<QR <= 4 ? 2 : 1>{}); break;
+      case 3: f(qr, IC<3>{}, IC<4>{}, IC<QR == 1 ? 2 : 1>{}); break;
+      default: f(qr, IC<4>{}, IC<4>{}, IC<QR == 1 ? 2 : 1>{});
+    }
+  };
+  if (rows <= 4) by_tiles(IC<1>{});
+  else if (rows <= 16) by_tiles(IC<4>{});
+  else by_tiles(IC<8>{});
+}
+
+template <int XT>
+static void dense_of_type(const void* x, int64_t ldx, const uint8_t* packed, const float* fscale,
+                          int M, int N, int K, OutY y, hipStream_t stream) {
+  const int passes = (M * kTerms<XT> + 31) / 32;
+  with_shape(M * kTerms<XT>, passes * (N / 16), [&](auto qr, auto nt, auto nw, auto d) {
+    launch_dense<XT, decltype(qr)::value, decltype(nt)::value, decltype(nw)::value,
+                 decltype(d)::value>(x, ldx, packed, fscale, M, N, K, y, stream);
+  });
+}
+
+template <int XT>
+static void routed_of_type(const void* x, int64_t ldx, const uint8_t* packed, const float* fscale,
+                           int N, int K, OutY y, const Route& rt, hipStream_t stream) {
+  // rows an expert gets at most, and half as many again as the mean: an expert
+  // with more takes another pass over its (cached) weights
+  const int busy = min(rt.E, rt.R);
+  const int rows = min(min(rt.T, rt.R), (3 * rt.R / rt.E + 1) / 2 + 1);
+  with_shape(rows * kTerms<XT>, busy * (N / 16), [&](auto qr, auto nt, auto nw, auto d) {
+    launch_routed<XT, decltype(qr)::value, decltype(nt)::value, decltype(nw)::value,
+                  decltype(d)::value>(x, ldx, packed, fscale, N, K, y, rt, stream);
+  });
 }
 
 hipError_t launch_w4a16(const void* x, int x_type, int64_t ldx, const uint8_t* packed,
                         const float* fscale, int64_t M, int64_t N, int64_t K, OutY y,
                         hipStream_t stream) {
-  const Route none{};
   const int m = (int)M, n = (int)N, k = (int)K;
-  if (x_type == kF32) launch_type<kF32, false>(x, ldx, packed, fscale, m, n, k, y, none, stream);
-  else if (x_type == kF16) launch_type<kF16, false>(x, ldx, packed, fscale, m, n, k, y, none, stream);
-  else launch_type<kBF16, false>(x, ldx, packed, fscale, m, n, k, y, none, stream);
+  if (x_type == kF32) dense_of_type<kF32>(x, ldx, packed, fscale, m, n, k, y, stream);
+  else if (x_type == kF16) dense_of_type<kF16>(x, ldx, packed, fscale, m, n, k, y, stream);
+  else dense_of_type<kBF16>(x, ldx, packed, fscale, m, n, k, y, stream);
   return hipGetLastError();
 }
 
@@ -244,11 +489,12 @@ hipError_t launch_w4a16_moe(const void* x, int x_type, int64_t ldx, int64_t T, c
                             const int32_t* tok, int64_t E, int64_t R, const uint8_t* packed,
                             const float* fscale, int64_t N, int64_t K, OutY y, hipStream_t stream) {
   const Route rt{offs, tok, (int)E, (int)T, (int)R, N * K / 2, (K / kGroup) * N};
-  const int m = (int)(T < R ? T : R), n = (int)N, k = (int)K;   // an expert's most rows
-  if (x_type == kF32) launch_type<kF32, true>(x, ldx, packed, fscale, m, n, k, y, rt, stream);
-  else if (x_type == kF16) launch_type<kF16, true>(x, ldx, packed, fscale, m, n, k, y, rt, stream);
-  else launch_type<kBF16, true>(x, ldx, packed, fscale, m, n, k, y, rt, stream);
+  const int n = (int)N, k = (int)K;
+  if (x_type == kF32) routed_of_type<kF32>(x, ldx, packed, fscale, n, k, y, rt, stream);
+  else if (x_type == kF16) routed_of_type<kF16>(x, ldx, packed, fscale, n, k, y, rt, stream);
+  else routed_of_type<kBF16>(x, ldx, packed, fscale, n, k, y, rt, stream);
   return hipGetLastError();
 }
+#endif
 
 }  // namespace bgt

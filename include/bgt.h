@@ -509,7 +509,7 @@ int bgt_moe_combine_backward(const void* dy, int64_t lddy, const void* ys, int t
  *           16-byte aligned.
  *   y       M x N of y_type, 16-byte aligned.
  * Requirements: M, N, K as bgt_w4a8_gemm_is. Any M is computed; the kernel
- * streams the weights once for up to 64 rows (21 of fp32) and again for each
+ * streams the weights once for up to 32 rows (10 of fp32) and again for each
  * further block of rows, so for many rows the W4A8 GEMMs are the faster way.
  */
 int bgt_w4a16_gemv(const void* x, int x_type, int64_t ldx, const uint8_t* packed,
