@@ -168,22 +168,38 @@ def w8a8_is_kernel_name(M: int, N: int, K: int) -> str:
 
 
 # ----------------------------------------------------------------- marshalling
+_torch_module = None
+_elem_codes = {}
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _elem_codes.update({torch.float32: BGT_F32, torch.float16: BGT_F16,
+                            torch.bfloat16: BGT_BF16})
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(device=None):
+    """torch's current HIP stream of the device, as an integer handle."""
     torch = _torch()
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is not None and device is not None and device.index is not None:
+        return raw(device.index)          # without building a Stream object (about 2 us)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _check(t, name, dtype, shape=None):
     torch = _torch()
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.is_contiguous() \
+            and (shape is None or t.shape == shape):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -198,11 +214,11 @@ def _check(t, name, dtype, shape=None):
 
 def _elem_type(t, name):
     """BGT element-type code of a float32 / float16 / bfloat16 tensor."""
-    torch = _torch()
-    codes = {torch.float32: BGT_F32, torch.float16: BGT_F16, torch.bfloat16: BGT_BF16}
-    if t.dtype not in codes:
+    _torch()
+    code = _elem_codes.get(t.dtype)
+    if code is None:
         raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
-    return codes[t.dtype]
+    return code
 
 
 def _raise(fn, st):
@@ -554,17 +570,22 @@ def _norm(norm):
     return _NORMS[norm]
 
 
+def _out(t, name, dtype, shape, dev):
+    """The output tensor given, checked, or a new one."""
+    if t is None:
+        return _torch().empty(*shape, dtype=dtype, device=dev)
+    _check(t, name, dtype, shape)
+    return t
+
+
 def _sort_buffers(T, E, k, dev, offs, tok, pos):
     """The sort's outputs (allocated where not given) and its workspace."""
     torch = _torch()
     need = lib().bgt_moe_sort_workspace_bytes(T, E, k)
     _raise("bgt_moe_sort_workspace_bytes", need if need < 0 else 0)
-    offs = torch.empty(E + 1, dtype=torch.int32, device=dev) if offs is None else offs
-    tok = torch.empty(T * k, dtype=torch.int32, device=dev) if tok is None else tok
-    pos = torch.empty((T, k), dtype=torch.int32, device=dev) if pos is None else pos
-    _check(offs, "offs", torch.int32, (E + 1,))
-    _check(tok, "tok", torch.int32, (T * k,))
-    _check(pos, "pos", torch.int32, (T, k))
+    offs = _out(offs, "offs", torch.int32, (E + 1,), dev)
+    tok = _out(tok, "tok", torch.int32, (T * k,), dev)
+    pos = _out(pos, "pos", torch.int32, (T, k), dev)
     ws = torch.empty(need // 4, dtype=torch.int32, device=dev) if need else None
     return offs, tok, pos, ws, need
 
@@ -583,10 +604,8 @@ def moe_route(logits, k: int, norm: str = "chosen", weights=None, ids=None, offs
     T, E, ld = _rows(logits, "logits")
     lt, nm, k, dev = _elem_type(logits, "logits"), _norm(norm), int(k), logits.device
     offs, tok, pos, ws, need = _sort_buffers(T, E, k, dev, offs, tok, pos)
-    weights = torch.empty((T, k), dtype=torch.float32, device=dev) if weights is None else weights
-    ids = torch.empty((T, k), dtype=torch.int32, device=dev) if ids is None else ids
-    _check(weights, "weights", torch.float32, (T, k))
-    _check(ids, "ids", torch.int32, (T, k))
+    weights = _out(weights, "weights", torch.float32, (T, k), dev)
+    ids = _out(ids, "ids", torch.int32, (T, k), dev)
     st = lib().bgt_moe_route(_ptr(logits), lt, ld, T, E, k, nm, _ptr(weights), _ptr(ids),
                              _ptr(offs), _ptr(tok), _ptr(pos), _ptr(ws), need, _stream(dev))
     _raise("bgt_moe_route", st)
@@ -618,9 +637,7 @@ def moe_route_backward(dweights, logits, ids, norm: str = "chosen", dlogits=None
         raise ValueError("ids must be T x k")
     k = ids.shape[1]
     _check(dweights, "dweights", torch.float32, (T, k))
-    if dlogits is None:
-        dlogits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    _check(dlogits, "dlogits", logits.dtype, (T, E))
+    dlogits = _out(dlogits, "dlogits", logits.dtype, (T, E), logits.device)
     st = lib().bgt_moe_route_backward(_ptr(dweights), _ptr(logits), lt, ld, _ptr(ids), T, E, k, nm,
                                       _ptr(dlogits), _stream(logits.device))
     _raise("bgt_moe_route_backward", st)
@@ -637,8 +654,7 @@ def moe_gather(x, offs, pos, xs=None):
     if pos.dim() != 2 or pos.shape[0] != T:
         raise ValueError("pos must be T x k")
     k = pos.shape[1]
-    xs = torch.empty((T * k, H), dtype=x.dtype, device=x.device) if xs is None else xs
-    _check(xs, "xs", x.dtype, (T * k, H))
+    xs = _out(xs, "xs", x.dtype, (T * k, H), x.device)
     st = lib().bgt_moe_gather(_ptr(x), xt, ld, _ptr(offs), _ptr(pos), T, offs.numel() - 1, k, H,
                               _ptr(xs), _stream(x.device))
     _raise("bgt_moe_gather", st)
@@ -660,8 +676,7 @@ def moe_combine(ys, pos, weights=None, y=None):
     H = ys.shape[1]
     if weights is not None:
         _check(weights, "weights", torch.float32, (T, k))
-    y = torch.empty((T, H), dtype=ys.dtype, device=ys.device) if y is None else y
-    _check(y, "y", ys.dtype, (T, H))
+    y = _out(y, "y", ys.dtype, (T, H), ys.device)
     st = lib().bgt_moe_combine(_ptr(ys), yt, _ptr(pos), _ptr(weights), T, k, H, _ptr(y),
                                _stream(ys.device))
     _raise("bgt_moe_combine", st)
@@ -686,11 +701,8 @@ def moe_combine_backward(dy, ys, offs, pos, weights, dys=None, dweights=None):
     k = pos.shape[1]
     _check(ys, "ys", dy.dtype, (T * k, H))
     _check(weights, "weights", torch.float32, (T, k))
-    dys = torch.empty_like(ys) if dys is None else dys
-    if dweights is None:
-        dweights = torch.empty((T, k), dtype=torch.float32, device=dy.device)
-    _check(dys, "dys", dy.dtype, (T * k, H))
-    _check(dweights, "dweights", torch.float32, (T, k))
+    dys = _out(dys, "dys", dy.dtype, (T * k, H), dy.device)
+    dweights = _out(dweights, "dweights", torch.float32, (T, k), dy.device)
     st = lib().bgt_moe_combine_backward(_ptr(dy), ld, _ptr(ys), yt, _ptr(offs), _ptr(pos),
                                         _ptr(weights), T, offs.numel() - 1, k, H, _ptr(dys),
                                         _ptr(dweights), _stream(dy.device))
@@ -708,9 +720,7 @@ def w4a16_gemv(x, packed, fscale, N: int, y=None, out_dtype=None):
     xt = _elem_type(x, "x")
     _check(packed, "packed", torch.uint8, (N * K // 2,))
     _check(fscale, "fscale", torch.float32, (K // GROUP, N))
-    if y is None:
-        y = torch.empty((M, N), dtype=out_dtype or x.dtype, device=x.device)
-    _check(y, "y", y.dtype, (M, N))
+    y = _out(y, "y", (out_dtype or x.dtype) if y is None else y.dtype, (M, N), x.device)
     st = lib().bgt_w4a16_gemv(_ptr(x), xt, ld, _ptr(packed), _ptr(fscale), M, N, K, _ptr(y),
                               _elem_type(y, "y"), _stream(x.device))
     _raise("bgt_w4a16_gemv", st)
@@ -729,9 +739,7 @@ def w4a16_moe_gemv(x, offsets, slot_token, packed, fscale, N: int, y=None, out_d
     E, R = offsets.numel() - 1, slot_token.numel()
     _check(packed, "packed", torch.uint8, (E, N * K // 2))
     _check(fscale, "fscale", torch.float32, (E, K // GROUP, N))
-    if y is None:
-        y = torch.empty((R, N), dtype=out_dtype or x.dtype, device=x.device)
-    _check(y, "y", y.dtype, (R, N))
+    y = _out(y, "y", (out_dtype or x.dtype) if y is None else y.dtype, (R, N), x.device)
     st = lib().bgt_w4a16_moe_gemv(_ptr(x), xt, ld, T, _ptr(offsets), _ptr(slot_token), E, R,
                                   _ptr(packed), _ptr(fscale), N, K, _ptr(y), _elem_type(y, "y"),
                                   _stream(x.device))

@@ -46,6 +46,19 @@ __device__ __forceinline__ float load_x1(const void* x, int64_t i) {
   else return __uint_as_float((uint32_t)static_cast<const uint16_t*>(x)[i] << 16);
 }
 
+// two fp32 values rounded to fp16 or bf16 (to nearest even) in one word
+template <int IT>
+__device__ __forceinline__ uint32_t narrow2(float a, float b) {
+  if constexpr (IT == kF16) {
+    const __half2 h = __halves2half2(__float2half(a), __float2half(b));
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __hip_bfloat16 x = __float2bfloat16(a), y = __float2bfloat16(b);
+    return (uint32_t)*reinterpret_cast<const uint16_t*>(&x) |
+           (uint32_t)*reinterpret_cast<const uint16_t*>(&y) << 16;
+  }
+}
+
 // The output matrix y and its element type. Values are computed in fp32 and
 // rounded once to the stored type (fp16, bf16: round to nearest even).
 struct OutY {

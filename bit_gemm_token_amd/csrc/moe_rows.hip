@@ -38,17 +38,6 @@ __device__ __forceinline__ void widen(const typename Chunk<IT, VEC>::T& u, float
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   }
 }
-template <int IT>
-__device__ __forceinline__ uint32_t narrow2(float a, float b) {
-  if constexpr (IT == kF16) {
-    const __half2 h = __halves2half2(__float2half(a), __float2half(b));
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    const __hip_bfloat16 x = __float2bfloat16(a), y = __float2bfloat16(b);
-    return (uint32_t)*reinterpret_cast<const uint16_t*>(&x) |
-           (uint32_t)*reinterpret_cast<const uint16_t*>(&y) << 16;
-  }
-}
 template <int IT, int VEC>
 __device__ __forceinline__ typename Chunk<IT, VEC>::T narrow(const float* v) {
   if constexpr (VEC == 1) {
