@@ -121,26 +121,30 @@ __device__ __forceinline__ uint4 lds_operand(const char* lds, int rb, int m) {
   return make_uint4(v.x, v.y, v.z, v.w);
 }
 
-// fp16 / bf16: 16 lanes a row
+// fp16 / bf16: 16 lanes a row. load() takes the next group; the pointers run
+// along (one pair of registers a quad; offsets from the group's number would
+// keep one for every step of an unrolled loop).
 template <int XT, int QR>
 struct Rows {
-  const uint16_t* x;             // at the lane's piece
-  int64_t ldx;
-  int row[QR];                   // row 4i + lane/16 of this pass, as a row of x
+  const uint16_t* row[QR];       // of row 4i + lane/16, at the lane's piece
   char* lds;
-  // slot(i): row index in x of row i of this pass (i < nr)
+  // slot(i): row index in x of row i of this pass (i < nr); g: the first group
   template <typename F>
-  __device__ __forceinline__ Rows(const void* xp, int64_t ld, int nr, char* block, F slot)
-      : x(static_cast<const uint16_t*>(xp) + 8 * (threadIdx.x % 16)), ldx(ld), lds(block) {
+  __device__ __forceinline__ Rows(const void* xp, int64_t ldx, int nr, char* block, int g, F slot)
+      : lds(block) {
+    const int lane = threadIdx.x % kWave;
 #pragma unroll
     for (int i = 0; i < QR; ++i)
-      row[i] = slot(min(4 * i + (int)(threadIdx.x % kWave) / 16, nr - 1));
+      row[i] = static_cast<const uint16_t*>(xp) + slot(min(4 * i + lane / 16, nr - 1)) * ldx +
+               (int64_t)g * kGroup + 8 * (lane % 16);
   }
   struct Raw { u4e v[QR]; };
-  __device__ __forceinline__ void load(Raw& r, int g) const {
+  __device__ __forceinline__ void load(Raw& r) {
 #pragma unroll
-    for (int i = 0; i < QR; ++i)
-      r.v[i] = *reinterpret_cast<const u4e*>(x + row[i] * ldx + (int64_t)g * kGroup);
+    for (int i = 0; i < QR; ++i) {
+      r.v[i] = *reinterpret_cast<const u4e*>(row[i]);
+      row[i] += kGroup;
+    }
   }
   __device__ __forceinline__ void stage(const Raw& r) const {
     const int lane = threadIdx.x % kWave;
@@ -163,18 +167,18 @@ struct Rows<kF32, QR> {
   int nr;
   char* lds;
   template <typename F>
-  __device__ __forceinline__ Rows(const void* xp, int64_t ldx, int rows, char* block, F slot)
-      : x(static_cast<const float*>(xp)), nr(rows), lds(block) {
+  __device__ __forceinline__ Rows(const void* xp, int64_t ldx, int rows, char* block, int g, F slot)
+      : x(static_cast<const float*>(xp) + (int64_t)g * kGroup), nr(rows), lds(block) {
 #pragma unroll
     for (int i = 0; i < ROWS; ++i)
       off[i] = (int64_t)__builtin_amdgcn_readfirstlane(slot(min(i, nr - 1))) * ldx;
   }
   struct Raw { f2e v[ROWS]; };
-  __device__ __forceinline__ void load(Raw& r, int g) const {
+  __device__ __forceinline__ void load(Raw& r) {
     const int lane = threadIdx.x % kWave;
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i)
-      r.v[i] = *reinterpret_cast<const f2e*>(x + off[i] + (int64_t)g * kGroup + 2 * lane);
+    for (int i = 0; i < ROWS; ++i) r.v[i] = reinterpret_cast<const f2e*>(x + off[i])[lane];
+    x += kGroup;
   }
   // v = hi + mid + lo by truncation, each exact in bf16 (its upper half); an
   // infinity or NaN stays whole in the first term (made quiet, so that its upper
@@ -210,13 +214,13 @@ struct Rows<kF32, QR> {
 // ------------------------------------------------------------------- kernel
 template <int QR> constexpr int kBlocks = (QR + 3) / 4;      // row blocks of 16
 
-// The wave's groups [gb, ge) of NT column tiles, D groups in flight.
+// The wave's groups [gb, ge) of NT column tiles.
 // make_rows() is called once the first weights have been requested (the row
 // list of routed slots is itself loaded).
-template <int XT, int QR, int NT, int D, typename F>
+template <int XT, int QR, int NT, typename F>
 __device__ __forceinline__ void run_groups(F make_rows, const uint4* __restrict__ packed,
                                            const float* __restrict__ fscale, int t0, int tiles,
-                                           int N, int G, int gb, int ge,
+                                           int N, int G, int gb, int ge, char* lds,
                                            v4f (&acc)[kBlocks<QR>][NT]) {
   constexpr int MR = kBlocks<QR>;
   const int lane = threadIdx.x % kWave, c = lane % 16;
@@ -229,65 +233,79 @@ __device__ __forceinline__ void run_groups(F make_rows, const uint4* __restrict_
     wp[nt] = packed + (int64_t)t * G * 64;
     sp[nt] = fscale + 16 * t;
   }
-  typename Rows<XT, QR>::Raw a[D];
-  uint4 w[D][NT];
-  float s[D][NT];
+  typename Rows<XT, QR>::Raw a;
+  uint4 w[2][NT];
+  float s[2][NT];
   auto load = [&](int u, int g) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const uint4* p = wp[nt] + (int64_t)g * 64 + lane;
-      w[u][nt] = *p;
+      w[u][nt] = (wp[nt] + (int64_t)g * 64)[lane];
       s[u][nt] = (sp[nt] + (int64_t)g * N)[c];
     }
   };
-  if (gb >= ge) return;
-#pragma unroll
-  for (int u = 0; u < D; ++u) load(u, min(gb + u, ge - 1));
-  const Rows<XT, QR> rows = make_rows();
-#pragma unroll
-  for (int u = 0; u < D; ++u) rows.load(a[u], min(gb + u, ge - 1));
+  // the four MFMAs of a group outermost: each operand is read once, and the
+  // NT * MR sums advance side by side
   auto compute = [&](int u) {
-    rows.stage(a[u]);
-    uint4 op[MR][4];
+    v4f p[MR][NT];
 #pragma unroll
-    for (int rb = 0; rb < MR; ++rb)
+    for (int m = 0; m < 4; ++m) {
+      uint4 op[MR];
 #pragma unroll
-      for (int m = 0; m < 4; ++m) op[rb][m] = lds_operand(rows.lds, rb, m);
+      for (int rb = 0; rb < MR; ++rb) op[rb] = lds_operand(lds, rb, m);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const uint4 b0 = unpack<XT>(w[u][nt].x), b1 = unpack<XT>(w[u][nt].y),
-                  b2 = unpack<XT>(w[u][nt].z), b3 = unpack<XT>(w[u][nt].w);
-      const float sc = s[u][nt] * kCodeScale<XT>;
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint4& q = w[u][nt];
+        const uint4 b = unpack<XT>(m == 0 ? q.x : m == 1 ? q.y : m == 2 ? q.z : q.w);
 #pragma unroll
-      for (int rb = 0; rb < MR; ++rb) {
-        v4f p = {0.0f, 0.0f, 0.0f, 0.0f};
-        p = mfma<XT>(op[rb][0], b0, p);
-        p = mfma<XT>(op[rb][1], b1, p);
-        p = mfma<XT>(op[rb][2], b2, p);
-        p = mfma<XT>(op[rb][3], b3, p);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[rb][nt][r] = __builtin_fmaf(p[r], sc, acc[rb][nt][r]);
+        for (int rb = 0; rb < MR; ++rb)
+          p[rb][nt] = mfma<XT>(op[rb], b, m == 0 ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : p[rb][nt]);
       }
     }
-  };
-  int g = gb;
-  for (; g + D < ge; g += D) {
 #pragma unroll
-    for (int u = 0; u < D; ++u) {
-      compute(u);
-      const int next = min(g + D + u, ge - 1);
-      load(u, next);
-      rows.load(a[u], next);
+    for (int nt = 0; nt < NT; ++nt) {
+      const float sc = s[u][nt] * kCodeScale<XT>;
+#pragma unroll
+      for (int rb = 0; rb < MR; ++rb)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[rb][nt][r] = __builtin_fmaf(p[rb][nt][r], sc, acc[rb][nt][r]);
+    }
+  };
+  if (gb >= ge) return;
+  load(0, gb);
+  Rows<XT, QR> rows = make_rows(gb, lds);
+  rows.load(a);
+  // A step hands its rows to LDS, requests the next group and computes its own,
+  // so one group is on its way while one is computed (two on their way measured
+  // no faster anywhere, and 6 to 12% slower with 16 rows: the registers cost
+  // waves). The loop's steps load without a condition, so that the compiler's
+  // wait counts are exact; the last one or two groups go through the tail.
+  int g = gb;
+  for (; g + 3 <= ge; g += 2) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      rows.stage(a);
+      load(u ^ 1, g + u + 1);
+      rows.load(a);
+      __builtin_amdgcn_sched_barrier(0);           // requests first, and no step's
+      compute(u);                                  // waits before the last one's work
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
-#pragma unroll
-  for (int u = 0; u < D; ++u)
-    if (g + u < ge) compute(u);
+  rows.stage(a);
+  if (g + 1 < ge) {
+    load(1, g + 1);
+    rows.load(a);
+    compute(0);
+    rows.stage(a);
+    compute(1);
+  } else {
+    compute(0);
+  }
 }
 
 // One workgroup: NT column tiles of 16 for up to 4*QR / terms rows; its NW
 // waves split the groups, and their partial outputs are added in wave order.
-template <int XT, int QR, int NT, int NW, int D>
+template <int XT, int QR, int NT, int NW>
 __device__ __forceinline__ void run_rows(char* lds, const void* x, int64_t ldx, const uint4* packed,
                                          const float* fscale, int N, int G, OutY y, const Route& rt,
                                          bool routed, int first, int nr) {
@@ -295,8 +313,8 @@ __device__ __forceinline__ void run_rows(char* lds, const void* x, int64_t ldx, 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const int c = lane % 16, s4 = lane / 16;
   const int t0 = blockIdx.x * NT;
-  auto make_rows = [&] {
-    return Rows<XT, QR>(x, ldx, nr, lds + wave * MR * 4096, [&](int i) {
+  auto make_rows = [&](int g, char* block) {
+    return Rows<XT, QR>(x, ldx, nr, block, g, [&](int i) {
       return routed ? clamp_route(rt.tok[first + i], 0, rt.T - 1) : first + i;
     });
   };
@@ -305,8 +323,8 @@ __device__ __forceinline__ void run_rows(char* lds, const void* x, int64_t ldx, 
   for (int rb = 0; rb < MR; ++rb)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) acc[rb][nt] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  run_groups<XT, QR, NT, D>(make_rows, packed, fscale, t0, N / 16, N, G, G * wave / NW,
-                            G * (wave + 1) / NW, acc);
+  run_groups<XT, QR, NT>(make_rows, packed, fscale, t0, N / 16, N, G, G * wave / NW,
+                            G * (wave + 1) / NW, lds + wave * MR * 4096, acc);
   float* part = reinterpret_cast<float*>(lds);     // [NW][16 MR][16 NT]
   __syncthreads();                                 // the waves' row blocks are done with
 #pragma unroll
@@ -335,14 +353,14 @@ template <int QR, int NT, int NW>
 constexpr int kLds = (NT < 4 ? 4 : NT) * 1024 * NW * kBlocks<QR>;
 
 // dense: up to 4*QR / terms rows a pass, grid z over the passes
-template <int XT, int QR, int NT, int NW, int D>
+template <int XT, int QR, int NT, int NW>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) void k_w4a16(
     const void* __restrict__ x, int64_t ldx, const uint4* __restrict__ packed,
     const float* __restrict__ fscale, int M, int N, int G, OutY y) {
   __shared__ __attribute__((aligned(16))) char lds[kLds<QR, NT, NW>];
   constexpr int ROWS = 4 * QR / kTerms<XT>;
   const int r0 = blockIdx.z * ROWS;
-  run_rows<XT, QR, NT, NW, D>(lds, x, ldx, packed, fscale, N, G, y, Route{}, false, r0,
+  run_rows<XT, QR, NT, NW>(lds, x, ldx, packed, fscale, N, G, y, Route{}, false, r0,
                               min(ROWS, M - r0));
 }
 
@@ -372,7 +390,7 @@ __device__ __forceinline__ bool busy_expert(const Route& rt, int j, int& e, int&
 // grid of a few slots has few rows); an expert's slots go through in passes of
 // up to 4*QR / terms rows (16 of A where that is enough). The first y zeroes
 // the rows past the last slot.
-template <int XT, int QR, int NT, int NW, int D>
+template <int XT, int QR, int NT, int NW>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) void k_w4a16_moe(
     const void* __restrict__ x, int64_t ldx, const uint4* __restrict__ packed,
     const float* __restrict__ fscale, int N, int G, OutY y, Route rt) {
@@ -390,40 +408,38 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) vo
   for (int r0 = 0, nr = 0; r0 < rows; r0 += nr) {
     nr = min(rows - r0, 4 * QR / TERMS);
     if (QR > 4 && nr * TERMS <= 16)
-      run_rows<XT, 4, NT, NW, D>(lds, x, ldx, packed, fscale, N, G, y, rt, true, first + r0, nr);
+      run_rows<XT, 4, NT, NW>(lds, x, ldx, packed, fscale, N, G, y, rt, true, first + r0, nr);
     else
-      run_rows<XT, QR, NT, NW, D>(lds, x, ldx, packed, fscale, N, G, y, rt, true, first + r0, nr);
+      run_rows<XT, QR, NT, NW>(lds, x, ldx, packed, fscale, N, G, y, rt, true, first + r0, nr);
   }
 }
 
-template <int XT, int QR, int NT, int NW, int D>
+template <int XT, int QR, int NT, int NW>
 static void launch_dense(const void* x, int64_t ldx, const uint8_t* packed, const float* fscale,
                          int M, int N, int K, OutY y, hipStream_t stream) {
   constexpr int ROWS = 4 * QR / kTerms<XT>;
   const int tiles = N / 16;
   const dim3 grid((tiles + NT - 1) / NT, 1, (M + ROWS - 1) / ROWS);
-  hipLaunchKernelGGL((k_w4a16<XT, QR, NT, NW, D>), grid, dim3(NW * 64), 0, stream, x, ldx,
+  hipLaunchKernelGGL((k_w4a16<XT, QR, NT, NW>), grid, dim3(NW * 64), 0, stream, x, ldx,
                      reinterpret_cast<const uint4*>(packed), fscale, M, N, K / kGroup, y);
 }
-template <int XT, int QR, int NT, int NW, int D>
+template <int XT, int QR, int NT, int NW>
 static void launch_routed(const void* x, int64_t ldx, const uint8_t* packed, const float* fscale,
                           int N, int K, OutY y, const Route& rt, hipStream_t stream) {
   const int tiles = N / 16;
-  hipLaunchKernelGGL((k_w4a16_moe<XT, QR, NT, NW, D>), dim3((tiles + NT - 1) / NT, min(rt.E, rt.R)),
+  hipLaunchKernelGGL((k_w4a16_moe<XT, QR, NT, NW>), dim3((tiles + NT - 1) / NT, min(rt.E, rt.R)),
                      dim3(NW * 64), 0, stream, x, ldx, reinterpret_cast<const uint4*>(packed),
                      fscale, N, K / kGroup, y, rt);
 }
 #ifndef BGT_GEMV_SWEEP
-// Column tiles a workgroup takes, for `tiles` tiles in the whole launch and QR
-// row quads: what the busiest CU then has to do, each workgroup's rows counted
-// as 0.3 tiles a quad. Sweeps (us), 2 / 3 / 4 tiles a workgroup: 16 x 4096 x
-// 22016 fp16 (1376 tiles) 13.9 / 11.9 / 14.9; 8 experts of 14336 x 4096, 61
-// tokens fp16 (2048 tiles) 71.5 / 69.1 / 55.0; 2 of 4096 x 14336, 1 token bf16
-// (1792 tiles) 15.1 / 17.6 / 14.4. Up to one tile a CU: 1 (1 x 4096 x 4096:
-// 3.5, with 2 tiles 5.1).
+// Column tiles a workgroup of more than one row quad takes, for `tiles` tiles in
+// the whole launch (more than one a CU): what the busiest CU then has to do,
+// each workgroup's rows counted as 0.3 tiles a quad. Sweeps (us), 1 / 2 / 3 / 4
+// tiles a workgroup: 16 x 4096 x 22016 fp16 (1376 tiles) 13.7 / 13.2 / 11.3 /
+// 12.8; 32 x 4096 x 22016 bf16 22.6 / 17.2 / 17.0 / 24.2; 8 experts of 14336 x
+// 4096, 61 tokens fp16 (2048 tiles) - / 73.8 / 72.1 / 65.4.
 static int tiles_per_wg(int tiles, int qr) {
   const int cus = device_cus();
-  if (tiles <= cus) return 1;
   int best = 2;
   float least = 0.0f;
   for (int nt = 2; nt <= 4; ++nt) {
@@ -434,21 +450,30 @@ static int tiles_per_wg(int tiles, int qr) {
   return best;
 }
 
-// f(QR, NT, NW, D) for rows of A and the tile count. One tile a workgroup gets
-// 8 waves, since there is then one workgroup a CU or fewer; two or more get 4.
-template <typename F>
+// f(QR, NT, NW) for rows of A and the tile count. Up to one tile a CU: a tile a
+// workgroup, its groups over 8 waves (16 for few fp32 rows, which have the
+// splitting to do: 3 x 11008 x 4096 10.7 -> 9.6 us). More: 4 waves, with one
+// tile for up to 4 rows of A, whose rows cost little (1 x 4096 x 11008 bf16, 1 /
+// 2 / 3 / 4 tiles: 6.2 / 7.9 / 7.3 / 8.7 us; 2 experts of 4096 x 14336, one
+// token: 12.5 / 13.9 / 14.1 / 14.2), else as tiles_per_wg says.
+template <int XT, typename F>
 static void with_shape(int rows, int tiles, F f) {
+  constexpr int FEW = XT == kF32 ? 16 : 8;
+  const bool one = tiles <= device_cus();
+  if (rows <= 4) {
+    if (one) f(IC<1>{}, IC<1>{}, IC<FEW>{});
+    else f(IC<1>{}, IC<1>{}, IC<4>{});
+    return;
+  }
   const auto by_tiles = [&](auto qr) {
     constexpr int QR = decltype(qr)::value;
-    switch (tiles_per_wg(tiles, QR)) {
-      case 1: f(qr, IC<1>{}, IC<8>{}, IC<QR <= 4 ? 2 : 1>{}); break;
-      case 2: f(qr, IC<2>{}, IC<4>{}, IC<QR <= 4 ? 2 : 1>{}); break;
-      case 3: f(qr, IC<3>{}, IC<4>{}, IC<QR == 1 ? 2 : 1>{}); break;
-      default: f(qr, IC<4>{}, IC<4>{}, IC<QR == 1 ? 2 : 1>{});
-    }
+    if (one) return f(qr, IC<1>{}, IC<QR <= 4 ? FEW : 8>{});
+    const int nt = tiles_per_wg(tiles, QR);
+    if (nt == 2) f(qr, IC<2>{}, IC<4>{});
+    else if (nt == 3) f(qr, IC<3>{}, IC<4>{});
+    else f(qr, IC<4>{}, IC<4>{});
   };
-  if (rows <= 4) by_tiles(IC<1>{});
-  else if (rows <= 16) by_tiles(IC<4>{});
+  if (rows <= 16) by_tiles(IC<4>{});
   else by_tiles(IC<8>{});
 }
 
@@ -456,9 +481,8 @@ template <int XT>
 static void dense_of_type(const void* x, int64_t ldx, const uint8_t* packed, const float* fscale,
                           int M, int N, int K, OutY y, hipStream_t stream) {
   const int passes = (M * kTerms<XT> + 31) / 32;
-  with_shape(M * kTerms<XT>, passes * (N / 16), [&](auto qr, auto nt, auto nw, auto d) {
-    launch_dense<XT, decltype(qr)::value, decltype(nt)::value, decltype(nw)::value,
-                 decltype(d)::value>(x, ldx, packed, fscale, M, N, K, y, stream);
+  with_shape<XT>(M * kTerms<XT>, passes * (N / 16), [&](auto qr, auto nt, auto nw) {
+    launch_dense<XT, decltype(qr)::value, decltype(nt)::value, decltype(nw)::value>(x, ldx, packed, fscale, M, N, K, y, stream);
   });
 }
 
@@ -469,9 +493,8 @@ static void routed_of_type(const void* x, int64_t ldx, const uint8_t* packed, co
   // with more takes another pass over its (cached) weights
   const int busy = min(rt.E, rt.R);
   const int rows = min(min(rt.T, rt.R), (3 * rt.R / rt.E + 1) / 2 + 1);
-  with_shape(rows * kTerms<XT>, busy * (N / 16), [&](auto qr, auto nt, auto nw, auto d) {
-    launch_routed<XT, decltype(qr)::value, decltype(nt)::value, decltype(nw)::value,
-                  decltype(d)::value>(x, ldx, packed, fscale, N, K, y, rt, stream);
+  with_shape<XT>(rows * kTerms<XT>, busy * (N / 16), [&](auto qr, auto nt, auto nw) {
+    launch_routed<XT, decltype(qr)::value, decltype(nt)::value, decltype(nw)::value>(x, ldx, packed, fscale, N, K, y, rt, stream);
   });
 }
 
