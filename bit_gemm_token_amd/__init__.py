@@ -578,16 +578,26 @@ def _out(t, name, dtype, shape, dev):
     return t
 
 
-def _sort_buffers(T, E, k, dev, offs, tok, pos):
-    """The sort's outputs (allocated where not given) and its workspace."""
+def _sort_buffers(T, E, k, dev, offs, tok, pos, ids=None, want_ids=False):
+    """The sort's outputs, its workspace and that one's size in bytes. Where the
+    caller gives no output they come from one allocation (an allocation costs
+    the host as much as the smallest kernels take)."""
     torch = _torch()
     need = lib().bgt_moe_sort_workspace_bytes(T, E, k)
     _raise("bgt_moe_sort_workspace_bytes", need if need < 0 else 0)
+    R = T * k
+    if offs is None and tok is None and pos is None and ids is None:
+        sizes = [E + 1, R, R, need // 4] + ([R] if want_ids else [])
+        block = torch.empty(sum(sizes), dtype=torch.int32, device=dev)
+        offs, tok, pos, ws, *rest = block.split_with_sizes(sizes)
+        return (offs, tok, pos.view(T, k), rest[0].view(T, k) if want_ids else None,
+                ws if need else None, need)
     offs = _out(offs, "offs", torch.int32, (E + 1,), dev)
-    tok = _out(tok, "tok", torch.int32, (T * k,), dev)
+    tok = _out(tok, "tok", torch.int32, (R,), dev)
     pos = _out(pos, "pos", torch.int32, (T, k), dev)
+    ids = _out(ids, "ids", torch.int32, (T, k), dev) if want_ids else None
     ws = torch.empty(need // 4, dtype=torch.int32, device=dev) if need else None
-    return offs, tok, pos, ws, need
+    return offs, tok, pos, ids, ws, need
 
 
 def moe_route(logits, k: int, norm: str = "chosen", weights=None, ids=None, offs=None, tok=None,
@@ -599,13 +609,13 @@ def moe_route(logits, k: int, norm: str = "chosen", weights=None, ids=None, offs
     the softmax over the chosen experts (norm "chosen") or over all ("all").
     Returns (weights, ids, offs, tok, pos): ids (T x k int32, -1 where too few
     experts were left), offs (E+1) and tok (T*k, -1 past offs[E]) as the grouped
-    products take them, pos (T x k) the sorted slot of each (token, expert)."""
+    products take them, pos (T x k) the sorted slot of each (token, expert).
+    Where none of ids, offs, tok and pos is given, they share one allocation."""
     torch = _torch()
     T, E, ld = _rows(logits, "logits")
     lt, nm, k, dev = _elem_type(logits, "logits"), _norm(norm), int(k), logits.device
-    offs, tok, pos, ws, need = _sort_buffers(T, E, k, dev, offs, tok, pos)
+    offs, tok, pos, ids, ws, need = _sort_buffers(T, E, k, dev, offs, tok, pos, ids, True)
     weights = _out(weights, "weights", torch.float32, (T, k), dev)
-    ids = _out(ids, "ids", torch.int32, (T, k), dev)
     st = lib().bgt_moe_route(_ptr(logits), lt, ld, T, E, k, nm, _ptr(weights), _ptr(ids),
                              _ptr(offs), _ptr(tok), _ptr(pos), _ptr(ws), need, _stream(dev))
     _raise("bgt_moe_route", st)
@@ -620,7 +630,7 @@ def moe_sort(ids, E: int, offs=None, tok=None, pos=None):
     if ids.dim() != 2:
         raise ValueError("ids must be 2-D")
     T, k = ids.shape
-    offs, tok, pos, ws, need = _sort_buffers(T, int(E), k, ids.device, offs, tok, pos)
+    offs, tok, pos, _, ws, need = _sort_buffers(T, int(E), k, ids.device, offs, tok, pos)
     st = lib().bgt_moe_sort(_ptr(ids), T, int(E), k, _ptr(offs), _ptr(tok), _ptr(pos), _ptr(ws),
                             need, _stream(ids.device))
     _raise("bgt_moe_sort", st)
