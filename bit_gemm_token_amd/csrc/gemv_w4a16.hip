@@ -388,7 +388,8 @@ __device__ __forceinline__ bool busy_expert(const Route& rt, int j, int& e, int&
 
 // routed: grid y counts the experts that have slots (at most one a slot, so the
 // grid of a few slots has few rows); an expert's slots go through in passes of
-// up to 4*QR / terms rows (16 of A where that is enough). The first y zeroes
+// up to 4*QR / terms rows, 16 or 24 rows of A where that is enough (8 experts of
+// 14336 x 4096 with 20 slots each: 58 us as 24 rows, 62 as 32). The first y zeroes
 // the rows past the last slot.
 template <int XT, int QR, int NT, int NW>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) void k_w4a16_moe(
@@ -409,6 +410,8 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) vo
     nr = min(rows - r0, 4 * QR / TERMS);
     if (QR > 4 && nr * TERMS <= 16)
       run_rows<XT, 4, NT, NW>(lds, x, ldx, packed, fscale, N, G, y, rt, true, first + r0, nr);
+    else if (QR > 6 && nr * TERMS <= 24)
+      run_rows<XT, 6, NT, NW>(lds, x, ldx, packed, fscale, N, G, y, rt, true, first + r0, nr);
     else
       run_rows<XT, QR, NT, NW>(lds, x, ldx, packed, fscale, N, G, y, rt, true, first + r0, nr);
   }
@@ -450,19 +453,22 @@ static int tiles_per_wg(int tiles, int qr) {
   return best;
 }
 
-// f(QR, NT, NW) for rows of A and the tile count. Up to one tile a CU: a tile a
-// workgroup, its groups over 8 waves (16 for few fp32 rows, which have the
-// splitting to do: 3 x 11008 x 4096 10.7 -> 9.6 us). More: 4 waves, with one
-// tile for up to 4 rows of A, whose rows cost little (1 x 4096 x 11008 bf16, 1 /
-// 2 / 3 / 4 tiles: 6.2 / 7.9 / 7.3 / 8.7 us; 2 experts of 4096 x 14336, one
-// token: 12.5 / 13.9 / 14.1 / 14.2), else as tiles_per_wg says.
+// f(QR, NT, NW) for rows of A, the tile count and the groups. Up to one tile a
+// CU: a tile a workgroup, its groups over 8 waves (16 for few fp32 rows, which
+// have the splitting to do: 3 x 11008 x 4096 10.7 -> 9.6 us). More: 4 waves, for
+// up to 4 rows of A, whose rows cost little, with one tile (1 x 4096 x 11008
+// bf16, 1 / 2 / 3 / 4 tiles: 6.2 / 7.9 / 7.3 / 8.7 us; 2 experts of 4096 x 14336,
+// one token: 12.5 / 13.9 / 14.1 / 14.2), in launches that stream 192 MiB and
+// more four (14336 x 32768: 61 with one, 47 with four; 14336 x 28672: 45 and 43;
+// below, 14336 x 22016: 35 and 38); for more rows as tiles_per_wg says.
 template <int XT, typename F>
-static void with_shape(int rows, int tiles, F f) {
+static void with_shape(int rows, int tiles, int groups, F f) {
   constexpr int FEW = XT == kF32 ? 16 : 8;
   const bool one = tiles <= device_cus();
   if (rows <= 4) {
     if (one) f(IC<1>{}, IC<1>{}, IC<FEW>{});
-    else f(IC<1>{}, IC<1>{}, IC<4>{});
+    else if ((int64_t)tiles * groups < 192 * 1024) f(IC<1>{}, IC<1>{}, IC<4>{});
+    else f(IC<1>{}, IC<4>{}, IC<4>{});
     return;
   }
   const auto by_tiles = [&](auto qr) {
@@ -481,7 +487,7 @@ template <int XT>
 static void dense_of_type(const void* x, int64_t ldx, const uint8_t* packed, const float* fscale,
                           int M, int N, int K, OutY y, hipStream_t stream) {
   const int passes = (M * kTerms<XT> + 31) / 32;
-  with_shape<XT>(M * kTerms<XT>, passes * (N / 16), [&](auto qr, auto nt, auto nw) {
+  with_shape<XT>(M * kTerms<XT>, passes * (N / 16), K / kGroup, [&](auto qr, auto nt, auto nw) {
     launch_dense<XT, decltype(qr)::value, decltype(nt)::value, decltype(nw)::value>(x, ldx, packed, fscale, M, N, K, y, stream);
   });
 }
@@ -493,7 +499,7 @@ static void routed_of_type(const void* x, int64_t ldx, const uint8_t* packed, co
   // with more takes another pass over its (cached) weights
   const int busy = min(rt.E, rt.R);
   const int rows = min(min(rt.T, rt.R), (3 * rt.R / rt.E + 1) / 2 + 1);
-  with_shape<XT>(rows * kTerms<XT>, busy * (N / 16), [&](auto qr, auto nt, auto nw) {
+  with_shape<XT>(rows * kTerms<XT>, busy * (N / 16), K / kGroup, [&](auto qr, auto nt, auto nw) {
     launch_routed<XT, decltype(qr)::value, decltype(nt)::value, decltype(nw)::value>(x, ldx, packed, fscale, N, K, y, rt, stream);
   });
 }

@@ -87,6 +87,31 @@ def test_dense(bgt, dev, M, K, N, kind):
     check(y, x, W)
 
 
+@pytest.mark.parametrize("M", [1, 5, 9, 30, 40])
+@pytest.mark.parametrize("tiles", [255, 257, 601, 901, 1100])
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_many_tiles(bgt, dev, M, tiles, kind):
+    # one to four column tiles a workgroup, the last one partly past the end, and
+    # group counts that the waves share unevenly
+    K, N = (384, 640, 128)[tiles % 3], 16 * tiles
+    say(f"gemv M={M} K={K} N={N} {kind}")
+    packed, s, W = weights(bgt, dev, M + tiles, K, N)
+    x = rows_of(M * K, M, K, TYPES[kind], dev)
+    check(bgt.w4a16_gemv(x, packed, s, N), x, W)
+
+
+@pytest.mark.parametrize("rows", [1, 4, 5, 16, 17, 24, 25, 32, 33, 70])
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_routed_row_counts(bgt, dev, rows, kind):
+    # one expert with `rows` slots beside experts with fewer: every row block size
+    # and several passes
+    say(f"moe gemv one expert with {rows} rows {kind}")
+    ids = np.full((rows, 1), 2, np.int32)
+    check_moe(bgt, dev, ids, 3, 256, 16 * 301, TYPES[kind], rows)
+    wide = np.stack([np.full(rows, 1), np.arange(rows) % 4 + 2], 1).astype(np.int32)
+    check_moe(bgt, dev, wide, 6, 640, 48, TYPES[kind], rows + 1)
+
+
 @pytest.mark.parametrize("kind", list(TYPES))
 @pytest.mark.parametrize("out", list(TYPES))
 def test_output_types_and_packer(bgt, dev, kind, out):
