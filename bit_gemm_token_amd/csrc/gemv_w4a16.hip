@@ -61,10 +61,15 @@ __device__ __forceinline__ uint32_t pack_hi(uint32_t hi, uint32_t lo) {
 template <int B>
 __device__ __forceinline__ uint32_t sixteenth(uint32_t w) {
   uint32_t f;
-  if constexpr (B == 0) asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_0" : "=v"(f) : "v"(w));
-  if constexpr (B == 1) asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_1" : "=v"(f) : "v"(w));
-  if constexpr (B == 2) asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_2" : "=v"(f) : "v"(w));
-  if constexpr (B == 3) asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_3" : "=v"(f) : "v"(w));
+#define BGT_SIXTEENTH(byte)                                                                 \
+  asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:" byte      \
+      : "=v"(f)                                                                             \
+      : "v"(w))
+  if constexpr (B == 0) BGT_SIXTEENTH("BYTE_0");
+  if constexpr (B == 1) BGT_SIXTEENTH("BYTE_1");
+  if constexpr (B == 2) BGT_SIXTEENTH("BYTE_2");
+  if constexpr (B == 3) BGT_SIXTEENTH("BYTE_3");
+#undef BGT_SIXTEENTH
   return f;
 }
 
@@ -90,8 +95,10 @@ __device__ __forceinline__ uint4 unpack(uint32_t w) {
                       __builtin_bit_cast(uint32_t, c), __builtin_bit_cast(uint32_t, d));
   } else {
     const uint32_t h = w >> 4;
-    return make_uint4(pack_hi(sixteenth<1>(w), sixteenth<0>(w)), pack_hi(sixteenth<3>(w), sixteenth<2>(w)),
-                      pack_hi(sixteenth<1>(h), sixteenth<0>(h)), pack_hi(sixteenth<3>(h), sixteenth<2>(h)));
+    return make_uint4(pack_hi(sixteenth<1>(w), sixteenth<0>(w)),
+                      pack_hi(sixteenth<3>(w), sixteenth<2>(w)),
+                      pack_hi(sixteenth<1>(h), sixteenth<0>(h)),
+                      pack_hi(sixteenth<3>(h), sixteenth<2>(h)));
   }
 }
 template <int XT> constexpr float kCodeScale = XT == kF16 ? 1.0f : 16.0f;
@@ -180,13 +187,11 @@ struct Rows<kF32, QR> {
     for (int i = 0; i < ROWS; ++i) r.v[i] = reinterpret_cast<const f2e*>(x + off[i])[lane];
     x += kGroup;
   }
-  // v = hi + mid + lo by truncation, each exact in bf16 (its upper half); an
-  // infinity or NaN stays whole in the first term (made quiet, so that its upper
-  // half is a NaN too)
+  // v = hi + mid + lo by truncation, each exact in bf16 (its upper half). An
+  // infinity stays whole in the first term; a NaN makes the second one NaN.
   __device__ __forceinline__ static void split(float v, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-    v = __builtin_canonicalizef(v);
     hi = __float_as_uint(v);
-    const float r1 = __builtin_isfinite(v) ? v - __uint_as_float(hi & 0xFFFF0000u) : 0.0f;
+    const float r1 = fabsf(v) == __builtin_inff() ? 0.0f : v - __uint_as_float(hi & 0xFFFF0000u);
     mid = __float_as_uint(r1);
     lo = __float_as_uint(r1 - __uint_as_float(mid & 0xFFFF0000u));
   }
@@ -267,7 +272,8 @@ __device__ __forceinline__ void run_groups(F make_rows, const uint4* __restrict_
 #pragma unroll
       for (int rb = 0; rb < MR; ++rb)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[rb][nt][r] = __builtin_fmaf(p[rb][nt][r], sc, acc[rb][nt][r]);
+        for (int r = 0; r < 4; ++r)
+          acc[rb][nt][r] = __builtin_fmaf(p[rb][nt][r], sc, acc[rb][nt][r]);
     }
   };
   if (gb >= ge) return;
@@ -342,7 +348,8 @@ __device__ __forceinline__ void run_rows(char* lds, const void* x, int64_t ldx, 
 #pragma unroll
       for (int w = 0; w < NW; ++w)
 #pragma unroll
-        for (int q = TERMS - 1; q >= 0; --q) v += part[(w * 16 * MR + i * TERMS + q) * (16 * NT) + j];
+        for (int q = TERMS - 1; q >= 0; --q)
+          v += part[(w * 16 * MR + i * TERMS + q) * (16 * NT) + j];
       y.put((int64_t)(first + i) * N + 16 * t0 + j, v);
     }
   }
@@ -374,7 +381,8 @@ __device__ __forceinline__ bool busy_expert(const Route& rt, int j, int& e, int&
     const unsigned long long busy = __ballot(base + lane < rt.E && b > a);
     const int n = __popcll(busy);
     if (j < n) {
-      const unsigned long long mine = __ballot(__popcll(busy & ((2ull << lane) - 1)) == j + 1) & busy;
+      const unsigned long long mine =
+          __ballot(__popcll(busy & ((2ull << lane) - 1)) == j + 1) & busy;
       const int l = __builtin_ctzll(mine);
       e = __builtin_amdgcn_readfirstlane(base + l);
       first = __builtin_amdgcn_readfirstlane(__shfl(a, l, kWave));
@@ -399,8 +407,9 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) vo
   constexpr int TERMS = kTerms<XT>;
   if (blockIdx.y == 0) {
     const int c0 = 16 * NT * blockIdx.x, cols = min(16 * NT, N - c0);
-    for (int r = clamp_route(rt.offs[rt.E], 0, rt.R); r < rt.R; ++r)
-      for (int j = threadIdx.x; j < cols; j += NW * 64) y.put((int64_t)r * N + c0 + j, 0.0f);
+    const int last = clamp_route(rt.offs[rt.E], 0, rt.R);
+    for (int64_t o = threadIdx.x; o < (int64_t)(rt.R - last) * cols; o += NW * 64)
+      y.put((last + o / cols) * N + c0 + o % cols, 0.0f);
   }
   int e, first, rows;
   if (!busy_expert(rt, blockIdx.y, e, first, rows)) return;
@@ -488,7 +497,8 @@ static void dense_of_type(const void* x, int64_t ldx, const uint8_t* packed, con
                           int M, int N, int K, OutY y, hipStream_t stream) {
   const int passes = (M * kTerms<XT> + 31) / 32;
   with_shape<XT>(M * kTerms<XT>, passes * (N / 16), K / kGroup, [&](auto qr, auto nt, auto nw) {
-    launch_dense<XT, decltype(qr)::value, decltype(nt)::value, decltype(nw)::value>(x, ldx, packed, fscale, M, N, K, y, stream);
+    launch_dense<XT, decltype(qr)::value, decltype(nt)::value, decltype(nw)::value>(
+        x, ldx, packed, fscale, M, N, K, y, stream);
   });
 }
 
@@ -500,7 +510,8 @@ static void routed_of_type(const void* x, int64_t ldx, const uint8_t* packed, co
   const int busy = min(rt.E, rt.R);
   const int rows = min(min(rt.T, rt.R), (3 * rt.R / rt.E + 1) / 2 + 1);
   with_shape<XT>(rows * kTerms<XT>, busy * (N / 16), K / kGroup, [&](auto qr, auto nt, auto nw) {
-    launch_routed<XT, decltype(qr)::value, decltype(nt)::value, decltype(nw)::value>(x, ldx, packed, fscale, N, K, y, rt, stream);
+    launch_routed<XT, decltype(qr)::value, decltype(nt)::value, decltype(nw)::value>(
+        x, ldx, packed, fscale, N, K, y, rt, stream);
   });
 }
 

@@ -165,7 +165,8 @@ __global__ __launch_bounds__(NW * 64) void k_slot_count(const int32_t* __restric
   __shared__ Sorter<NW> sh;
   const int64_t s0 = blockIdx.x * chunk;
   sh.count(ids, s0, min(R, s0 + chunk), E);
-  for (int e = threadIdx.x; e < E; e += NW * kWave) counts[(int64_t)blockIdx.x * E + e] = sh.counted(e);
+  for (int e = threadIdx.x; e < E; e += NW * kWave)
+    counts[(int64_t)blockIdx.x * E + e] = sh.counted(e);
 }
 
 // chunk b's slots, given every chunk's counts. The threads add up the counts
@@ -203,7 +204,8 @@ __global__ __launch_bounds__(NW * 64) void k_slot_place(const int32_t* __restric
   __syncthreads();
   sh.scan(totals, before, E, b == 0 ? offs : nullptr);
   sh.place(ids, s0, s1, E, k, tok, pos);
-  for (int64_t r = sh.total + (int64_t)b * NW * kWave + threadIdx.x; r < R; r += (int64_t)n * NW * kWave)
+  for (int64_t r = sh.total + (int64_t)b * NW * kWave + threadIdx.x; r < R;
+       r += (int64_t)n * NW * kWave)
     tok[r] = -1;
 }
 
@@ -225,7 +227,8 @@ __device__ __forceinline__ void load_logits(const void* row, int e0, int E, floa
         v[4 * q] = __uint_as_float(u.x); v[4 * q + 1] = __uint_as_float(u.y);
         v[4 * q + 2] = __uint_as_float(u.z); v[4 * q + 3] = __uint_as_float(u.w);
       } else {
-        const float4 a = widen_x4<IT>(make_uint2(u.x, u.y)), b = widen_x4<IT>(make_uint2(u.z, u.w));
+        const float4 a = widen_x4<IT>(make_uint2(u.x, u.y));
+        const float4 b = widen_x4<IT>(make_uint2(u.z, u.w));
         v[8 * q] = a.x; v[8 * q + 1] = a.y; v[8 * q + 2] = a.z; v[8 * q + 3] = a.w;
         v[8 * q + 4] = b.x; v[8 * q + 5] = b.y; v[8 * q + 6] = b.z; v[8 * q + 7] = b.w;
       }
@@ -241,10 +244,11 @@ __device__ __forceinline__ void load_logits(const void* row, int e0, int E, floa
 // hold the same), the other 16. Up to 16 lanes these are register moves.
 template <int STEP>
 __device__ __forceinline__ int partner(int v) {
-  if constexpr (STEP == 1) return __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, true);    // quad 1,0,3,2
-  else if constexpr (STEP == 2) return __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, true);  // quad 2,3,0,1
-  else if constexpr (STEP == 4) return __builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, true); // mirror of 8
-  else if constexpr (STEP == 8) return __builtin_amdgcn_update_dpp(0, v, 0x140, 0xF, 0xF, true); // mirror of 16
+  // DPP controls: quad permutations 1,0,3,2 and 2,3,0,1, mirrors of 8 and of 16
+  if constexpr (STEP == 1) return __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, true);
+  else if constexpr (STEP == 2) return __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, true);
+  else if constexpr (STEP == 4) return __builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, true);
+  else if constexpr (STEP == 8) return __builtin_amdgcn_update_dpp(0, v, 0x140, 0xF, 0xF, true);
   else return __shfl_xor(v, STEP, kWave);
 }
 template <int STEP>
@@ -299,7 +303,8 @@ __global__ __launch_bounds__(kTopWaves<L> * 64) void k_route_top(
     const int64_t t = tr + mine;
     float v[V];
     if (t < t1) {
-      load_logits<IT, V>(static_cast<const char*>(logits) + t * ld * (IT == kF32 ? 4 : 2), V * l, E, v);
+      const char* row = static_cast<const char*>(logits) + t * ld * (IT == kF32 ? 4 : 2);
+      load_logits<IT, V>(row, V * l, E, v);
     } else {
 #pragma unroll
       for (int j = 0; j < V; ++j) v[j] = kNegInf;
@@ -346,7 +351,8 @@ __global__ __launch_bounds__(kTopWaves<L> * 64) void k_route_top(
     __syncthreads();
   }
   if (chunk_counts) {
-    for (int e = threadIdx.x; e < E; e += THREADS) chunk_counts[(int64_t)blockIdx.x * E + e] = sh.base[e];
+    for (int e = threadIdx.x; e < E; e += THREADS)
+      chunk_counts[(int64_t)blockIdx.x * E + e] = sh.base[e];
   } else {
     sh.sort_all(ids, T * k, E, k, offs, tok, pos);
   }
@@ -371,7 +377,8 @@ __global__ __launch_bounds__(256) void k_route_grad(const float* __restrict__ dw
   }
   float v[V], d[V];
   if (in) {
-    load_logits<IT, V>(static_cast<const char*>(logits) + t * ld * (IT == kF32 ? 4 : 2), V * l, E, v);
+    const char* row = static_cast<const char*>(logits) + t * ld * (IT == kF32 ? 4 : 2);
+    load_logits<IT, V>(row, V * l, E, v);
   } else {
 #pragma unroll
     for (int j = 0; j < V; ++j) v[j] = kNegInf;
@@ -424,8 +431,8 @@ __global__ __launch_bounds__(256) void k_route_grad(const float* __restrict__ dw
     for (int q = 0; q < V / W; ++q) {
       u4e u;
       if constexpr (IT == kF32)
-        u = u4e{__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
-                __float_as_uint(v[4 * q + 3])};
+        u = u4e{__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3])};
       else
         u = u4e{narrow2<IT>(v[8 * q], v[8 * q + 1]), narrow2<IT>(v[8 * q + 2], v[8 * q + 3]),
                 narrow2<IT>(v[8 * q + 4], v[8 * q + 5]), narrow2<IT>(v[8 * q + 6], v[8 * q + 7])};
@@ -452,7 +459,10 @@ void with_lanes(int E, F f) {
 }
 int tokens_at_once(int E) {
   int n = 0;
-  with_lanes(E, [&](auto lanes, auto) { n = kTopWaves<decltype(lanes)::value> * kWave / decltype(lanes)::value; });
+  with_lanes(E, [&](auto lanes, auto) {
+    constexpr int L = decltype(lanes)::value;
+    n = kTopWaves<L> * kWave / L;
+  });
   return n;
 }
 
@@ -523,9 +533,10 @@ hipError_t launch_moe_route(const void* logits, int type, int64_t ld, int64_t T,
   const int64_t tb = single ? T : chunk_tokens(T, E);
   int32_t* counts = single ? nullptr : ws;
   const int e = (int)E, n = (int)k;
-  if (type == kF32) launch_top<kF32>(logits, ld, T, tb, e, n, all, weights, ids, counts, offs, tok, pos, stream);
-  else if (type == kF16) launch_top<kF16>(logits, ld, T, tb, e, n, all, weights, ids, counts, offs, tok, pos, stream);
-  else launch_top<kBF16>(logits, ld, T, tb, e, n, all, weights, ids, counts, offs, tok, pos, stream);
+  const auto top = type == kF32   ? launch_top<kF32>
+                   : type == kF16 ? launch_top<kF16>
+                                  : launch_top<kBF16>;
+  top(logits, ld, T, tb, e, n, all, weights, ids, counts, offs, tok, pos, stream);
   if (!single) launch_place(ids, T * k, tb * k, e, n, ws, offs, tok, pos, stream);
   return hipGetLastError();
 }

@@ -21,6 +21,7 @@ namespace bgt {
 
 constexpr int kRowThreads = 256;
 constexpr int kTailBlocks = 64;       // workgroups that zero the slots past the last one
+constexpr int64_t kMostBlocks = 1 << 20;
 
 typedef uint32_t u4e __attribute__((ext_vector_type(4), aligned(2)));   // 16 bytes, element-aligned
 
@@ -57,7 +58,8 @@ __device__ __forceinline__ void store_piece(void* m, int64_t row, int64_t ld, in
   if constexpr (WHOLE) {
     u4e u;
     if constexpr (IT == kF32)
-      u = u4e{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+      u = u4e{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+              __float_as_uint(v[3])};
     else
       u = u4e{narrow2<IT>(v[0], v[1]), narrow2<IT>(v[2], v[3]), narrow2<IT>(v[4], v[5]),
               narrow2<IT>(v[6], v[7])};
@@ -86,6 +88,19 @@ __device__ __forceinline__ void for_pieces(int l, int lanes, int H, F f) {
   }
 }
 
+// f(whole, t, h) for all pieces that this thread takes: `blocks` workgroups of
+// 256 >> sh tokens, 1 << sh lanes each, grid y splitting a token's row further.
+// A launch has at most kMostBlocks of them (a grid's threads are counted in 32
+// bits), hence the loop over tokens.
+template <int VEC, typename F>
+__device__ __forceinline__ void for_tokens(int blocks, int64_t tokens, int sh, int H, F f) {
+  const int lanes = 1 << sh, l = threadIdx.x & (lanes - 1);
+  const int64_t each = 256 >> sh;
+  for (int64_t t = blockIdx.x * each + (threadIdx.x >> sh); t < tokens; t += blocks * each)
+    for_pieces<VEC>(blockIdx.y * lanes + l, gridDim.y * lanes, H,
+                    [&](auto whole, int h, int) { f(whole, t, h); });
+}
+
 // zero the slots from the last expert's end to R (workgroup b of kTailBlocks);
 // T is the element's type
 template <typename T>
@@ -97,8 +112,7 @@ __device__ __forceinline__ void zero_tail(const int32_t* offs, int E, int64_t R,
     out[o] = 0;
 }
 
-// Workgroup: 256 >> sh tokens of 1 << sh lanes; grid y splits long rows of few
-// tokens. The last kTailBlocks workgroups zero the tail.
+// The last kTailBlocks workgroups zero the tail.
 template <typename T>
 __global__ __launch_bounds__(kRowThreads) void k_moe_gather(const T* __restrict__ x, int64_t ld,
                                                             const int32_t* __restrict__ offs,
@@ -112,10 +126,7 @@ __global__ __launch_bounds__(kRowThreads) void k_moe_gather(const T* __restrict_
     if (blockIdx.y == 0) zero_tail<T>(offs, E, R, H, xs, tail);
     return;
   }
-  const int64_t t = ((int64_t)blockIdx.x << (8 - sh)) + (threadIdx.x >> sh);
-  if (t >= tokens) return;
-  const int lanes = 1 << sh, l = threadIdx.x & (lanes - 1);
-  for_pieces<VEC>(blockIdx.y * lanes + l, gridDim.y * lanes, H, [&](auto whole, int h, int skip) {
+  for_tokens<VEC>(gridDim.x - kTailBlocks, tokens, sh, H, [&](auto whole, int64_t t, int h) {
     const T* src = x + t * ld + h;
     u4e v{};
     if constexpr (decltype(whole)::value) v = *reinterpret_cast<const u4e*>(src);
@@ -130,10 +141,11 @@ __global__ __launch_bounds__(kRowThreads) void k_moe_gather(const T* __restrict_
   });
 }
 
-// AT: expert rows of a token in flight together. Near the rate of a copy: 4096 x
-// 4096 bf16, k = 2: gather 16.3 us (100 MB), its gradient and combine alike,
-// combine's gradient 33.8 us (168 MB, 5.0 TB/s; a copy moves 5.2). A dropped place reads row 0 and
-// uses none of it, which costs less than a branch around the load.
+// AT: expert rows of a token in flight together. A dropped place reads row 0 and
+// uses none of it, which costs less than a branch around the load. All three
+// kernels run near the rate of a copy (5.2 TB/s): 4096 x 4096 bf16, k = 2, gather
+// 16.0 us (100 MB, partly from the Infinity Cache), combine's gradient 34 us (168
+// MB).
 template <int IT, int AT>
 __global__ __launch_bounds__(kRowThreads) void k_moe_combine(const void* __restrict__ ys,
                                                              const int32_t* __restrict__ pos,
@@ -141,10 +153,8 @@ __global__ __launch_bounds__(kRowThreads) void k_moe_combine(const void* __restr
                                                              int64_t tokens, int k, int H, int sh,
                                                              void* __restrict__ y) {
   constexpr int VEC = Elem<IT>::VEC;
-  const int64_t R = tokens * k, t = ((int64_t)blockIdx.x << (8 - sh)) + (threadIdx.x >> sh);
-  if (t >= tokens) return;
-  const int lanes = 1 << sh, l = threadIdx.x & (lanes - 1);
-  for_pieces<VEC>(blockIdx.y * lanes + l, gridDim.y * lanes, H, [&](auto whole, int h, int skip) {
+  const int64_t R = tokens * k;
+  for_tokens<VEC>(gridDim.x, tokens, sh, H, [&](auto whole, int64_t t, int h) {
     constexpr bool WHOLE = decltype(whole)::value;
     float acc[VEC] = {};
     for (int i0 = 0; i0 < k; i0 += AT) {
@@ -186,61 +196,65 @@ __global__ __launch_bounds__(kRowThreads) void k_moe_combine_grad(
   const int tail = (int)(blockIdx.x + kTailBlocks) - (int)gridDim.x;
   if (tail >= 0)
     return zero_tail(offs, E, R, H, static_cast<typename Elem<IT>::T*>(dys), tail);
-  const int64_t t = ((int64_t)blockIdx.x << (8 - sh)) + (threadIdx.x >> sh);
-  const bool in = t < tokens;
   const int lanes = 1 << sh, l = threadIdx.x & (lanes - 1);
-  for (int i0 = 0; i0 < k; i0 += AT) {
-    float wi[AT], dot[AT];
-    int p[AT];
-    bool ok[AT];
+  const int64_t each = 256 >> sh, stride = (gridDim.x - kTailBlocks) * each;
+  // the same count of rounds for all threads (they meet at barriers)
+  for (int64_t t0 = blockIdx.x * each; t0 < tokens; t0 += stride) {
+    for (int i0 = 0; i0 < k; i0 += AT) {
+      const int64_t t = t0 + (threadIdx.x >> sh);
+      const bool in = t < tokens;
+      float wi[AT], dot[AT];
+      int p[AT];
+      bool ok[AT];
 #pragma unroll
-    for (int j = 0; j < AT; ++j) {
-      ok[j] = false;
-      p[j] = 0;
-      wi[j] = dot[j] = 0.0f;
-      if (in && i0 + j < k) {
-        p[j] = pos[t * k + i0 + j];
-        ok[j] = p[j] >= 0 && p[j] < R;
-        if (!ok[j]) p[j] = 0;
-        wi[j] = w[t * k + i0 + j];
+      for (int j = 0; j < AT; ++j) {
+        ok[j] = false;
+        p[j] = 0;
+        wi[j] = dot[j] = 0.0f;
+        if (in && i0 + j < k) {
+          p[j] = pos[t * k + i0 + j];
+          ok[j] = p[j] >= 0 && p[j] < R;
+          if (!ok[j]) p[j] = 0;
+          wi[j] = w[t * k + i0 + j];
+        }
       }
-    }
-    if (in)
-      for_pieces<VEC>(l, lanes, H, [&](auto whole, int h, int skip) {
-        constexpr bool WHOLE = decltype(whole)::value;
-        float g[VEC], v[AT][VEC];
-        load_piece<IT, WHOLE>(dy, t, ld, h, H, g);
+      if (in)
+        for_pieces<VEC>(l, lanes, H, [&](auto whole, int h, int skip) {
+          constexpr bool WHOLE = decltype(whole)::value;
+          float g[VEC], v[AT][VEC];
+          load_piece<IT, WHOLE>(dy, t, ld, h, H, g);
 #pragma unroll
-        for (int j = 0; j < AT; ++j)
-          if (i0 + j < k) load_piece<IT, WHOLE>(ys, p[j], H, h, H, v[j]);       // uniform
+          for (int j = 0; j < AT; ++j)
+            if (i0 + j < k) load_piece<IT, WHOLE>(ys, p[j], H, h, H, v[j]);       // uniform
 #pragma unroll
-        for (int j = 0; j < AT; ++j)
-          if (i0 + j < k) {
+          for (int j = 0; j < AT; ++j)
+            if (i0 + j < k) {
 #pragma unroll
-            for (int c = 0; c < VEC; ++c) {
-              if (ok[j] && c >= skip) dot[j] = __builtin_fmaf(g[c], v[j][c], dot[j]);
-              v[j][c] = g[c] * wi[j];
+              for (int c = 0; c < VEC; ++c) {
+                if (ok[j] && c >= skip) dot[j] = __builtin_fmaf(g[c], v[j][c], dot[j]);
+                v[j][c] = g[c] * wi[j];
+              }
+              if (ok[j]) store_piece<IT, WHOLE>(dys, p[j], H, h, H, v[j]);
             }
-            if (ok[j]) store_piece<IT, WHOLE>(dys, p[j], H, h, H, v[j]);
-          }
-      });
-    for (int o = 1; o < min(lanes, kWave); o <<= 1)
+        });
+      for (int o = 1; o < min(lanes, kWave); o <<= 1)
 #pragma unroll
-      for (int j = 0; j < AT; ++j) dot[j] += __shfl_xor(dot[j], o, kWave);
-    if (sh == 8) {
-      __syncthreads();                             // the last round's sums are read
+        for (int j = 0; j < AT; ++j) dot[j] += __shfl_xor(dot[j], o, kWave);
+      if (sh == 8) {
+        __syncthreads();                             // the last round's sums are read
 #pragma unroll
-      for (int j = 0; j < AT; ++j)
-        if (threadIdx.x % kWave == 0) sums[threadIdx.x / kWave][j] = dot[j];
-      __syncthreads();
+        for (int j = 0; j < AT; ++j)
+          if (threadIdx.x % kWave == 0) sums[threadIdx.x / kWave][j] = dot[j];
+        __syncthreads();
 #pragma unroll
-      for (int j = 0; j < AT; ++j)
-        dot[j] = ((sums[0][j] + sums[1][j]) + sums[2][j]) + sums[3][j];
+        for (int j = 0; j < AT; ++j)
+          dot[j] = ((sums[0][j] + sums[1][j]) + sums[2][j]) + sums[3][j];
+      }
+      if (in && l == 0)
+#pragma unroll
+        for (int j = 0; j < AT; ++j)
+          if (i0 + j < k) dw[t * k + i0 + j] = dot[j];
     }
-    if (in && l == 0)
-#pragma unroll
-      for (int j = 0; j < AT; ++j)
-        if (i0 + j < k) dw[t * k + i0 + j] = dot[j];
   }
 }
 
@@ -255,7 +269,8 @@ int lanes_log2(int64_t pieces, int most) {
 }
 unsigned token_blocks(int64_t T, int sh) {
   const int64_t each = 256 >> sh;
-  return (unsigned)((T + each - 1) / each);
+  const int64_t blocks = (T + each - 1) / each;
+  return (unsigned)(blocks < kMostBlocks ? blocks : kMostBlocks);
 }
 // workgroups along a row: rows longer than one workgroup's pieces are split
 // where there are fewer workgroups than CUs
@@ -300,8 +315,8 @@ hipError_t launch_moe_combine(const void* ys, int type, const int32_t* pos, cons
   const int sh = lanes_log2(pieces, 8);
   const unsigned blocks = token_blocks(T, sh);
   with_type(type, k <= 2, [&](auto it, auto at) {
-    hipLaunchKernelGGL((k_moe_combine<decltype(it)::value, decltype(at)::value>), dim3(blocks, row_blocks(pieces, blocks)),
-                       dim3(kRowThreads), 0, stream, ys, pos, weights, T, (int)k, (int)H, sh, y);
+    hipLaunchKernelGGL((k_moe_combine<decltype(it)::value, decltype(at)::value>),
+                       dim3(blocks, row_blocks(pieces, blocks)), dim3(kRowThreads), 0, stream, ys, pos, weights, T, (int)k, (int)H, sh, y);
   });
   return hipGetLastError();
 }

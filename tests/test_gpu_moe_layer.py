@@ -50,7 +50,8 @@ def test_served(layer, T, bound):
 
     def unpacked(name, ws):
         scale = served.parts[name][1].double().repeat_interleave(128, 1)
-        return torch.round(ws.double() / scale).clamp(-7, 7) * scale
+        v = (ws / scale.float()).double()                      # half away from zero, as the packer
+        return (torch.sign(v) * torch.floor(v.abs() + 0.5)).clamp(-7, 7) * scale
 
     ref = plain(x.double(), logits.double(), unpacked("gate", gate), unpacked("up", up),
                 unpacked("down", down), k)

@@ -201,6 +201,23 @@ def test_offsets_past_32_bits(bgt, dev):
     assert ((dw[t].double() - ref[:, None]).abs() <= (H / 32 + 32) * U * ref[:, None]).all()
 
 
+def test_more_tokens_than_a_launch_has_workgroups(bgt, dev):
+    # over 2^20 workgroups' worth of tokens (a workgroup a token at this length)
+    T, H, E, k = (1 << 20) + 4099, 1032, 4, 1
+    ids = (torch.arange(T, device=dev) * 7 % E).to(torch.int32).view(T, 1)
+    offs, tok, pos = bgt.moe_sort(ids, E)
+    x = (torch.arange(T, device=dev, dtype=torch.int32) % 251).to(torch.bfloat16)[:, None].expand(T, H).contiguous()
+    xs = bgt.moe_gather(x, offs, pos)
+    assert torch.equal(xs[:, 0], x[tok.long(), 0]) and torch.equal(xs[:, -1], x[tok.long(), 0])
+    w = (torch.arange(T, device=dev) % 3).float().view(T, 1)
+    y = bgt.moe_combine(xs, pos, w)
+    assert torch.equal(y[:, 5].float(), (x[:, 0].float() * w[:, 0]).to(torch.bfloat16).float())
+    dys, dw = bgt.moe_combine_backward(x, xs, offs, pos, w)
+    assert torch.equal(dys[pos[:, 0].long(), H - 1], y[:, 5])
+    assert torch.equal(dw[:, 0], x[:, 0].float() ** 2 * H)      # whole numbers below 2^24 * 4: exact
+    assert xs.shape[0] > 1 << 20
+
+
 def test_other_stream_and_graph(bgt, dev):
     T, H, E, k = 300, 520, 8, 2
     offs, tok, pos = routing(bgt, dev, T, E, k, 11)

@@ -117,9 +117,10 @@ def test_routed_row_counts(bgt, dev, rows, kind):
 def test_output_types_and_packer(bgt, dev, kind, out):
     # the packer's own codes and scales
     M, K, N = 7, 1024, 304
-    w = 0.02 * torch.randn(K, N, device=dev)
+    w = 0.02 * torch.randn(K, N, generator=torch.Generator(device=dev).manual_seed(1), device=dev)
     pw = bgt.pack_weights_int4(w)
-    q = torch.round(w.view(K // 128, 128, N) / pw["fscale"][:, None]).view(K, N)
+    v = (w.view(K // 128, 128, N) / pw["fscale"][:, None]).view(K, N).double()
+    q = torch.sign(v) * torch.floor(v.abs() + 0.5)           # half away from zero, as the packer
     W = q.double() * pw["fscale"].double().repeat_interleave(128, 0)
     x = rows_of(3, M, K, TYPES[kind], dev)
     y = bgt.w4a16_gemv(x, pw["packed"], pw["fscale"], N, out_dtype=TYPES[out])
@@ -175,6 +176,9 @@ def test_infinities_and_nan_stay_in_their_rows(bgt, dev, kind):
     assert torch.isfinite(y[fine]).all()
     assert torch.equal(y[fine], bgt.w4a16_gemv(x.nan_to_num(0, 0, 0), packed, s, N).double()[fine])
     assert torch.isnan(y[11]).all()
+    if kind == "f32":                              # a signaling NaN, its payload in the low bits only
+        x[11, 300] = torch.tensor(0x7F800001, dtype=torch.int32).view(torch.float32)
+        assert torch.isnan(bgt.w4a16_gemv(x, packed, s, N)[11]).all()
     for row, k, sign in ((4, 100, 1), (18, 7, -1)):
         w = W[k]                                   # inf times a code: its sign, or NaN for 0
         assert torch.equal(torch.isnan(y[row]), w == 0)
