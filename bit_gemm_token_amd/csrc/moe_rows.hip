@@ -184,7 +184,8 @@ __global__ __launch_bounds__(kRowThreads) void k_moe_combine(const void* __restr
 }
 
 // A token's lanes are part of one wave, or the whole workgroup (sh = 8), whose
-// waves' sums then meet in LDS.
+// waves' sums then meet in LDS. Grid y deals a token's places out, AT at a time; a
+// place's sum has the same order whichever workgroup takes it.
 template <int IT, int AT>
 __global__ __launch_bounds__(kRowThreads) void k_moe_combine_grad(
     const void* __restrict__ dy, int64_t ld, const void* __restrict__ ys,
@@ -194,13 +195,14 @@ __global__ __launch_bounds__(kRowThreads) void k_moe_combine_grad(
   __shared__ float sums[WAVES][AT];
   const int64_t R = tokens * k;
   const int tail = (int)(blockIdx.x + kTailBlocks) - (int)gridDim.x;
+  if (tail >= 0 && blockIdx.y > 0) return;
   if (tail >= 0)
     return zero_tail(offs, E, R, H, static_cast<typename Elem<IT>::T*>(dys), tail);
   const int lanes = 1 << sh, l = threadIdx.x & (lanes - 1);
   const int64_t each = 256 >> sh, stride = (gridDim.x - kTailBlocks) * each;
   // the same count of rounds for all threads (they meet at barriers)
   for (int64_t t0 = blockIdx.x * each; t0 < tokens; t0 += stride) {
-    for (int i0 = 0; i0 < k; i0 += AT) {
+    for (int i0 = AT * blockIdx.y; i0 < k; i0 += AT * gridDim.y) {
       const int64_t t = t0 + (threadIdx.x >> sh);
       const bool in = t < tokens;
       float wi[AT], dot[AT];
@@ -328,14 +330,22 @@ hipError_t launch_moe_combine_backward(const void* dy, int64_t ld, const void* y
   const int64_t pieces = pieces_of(type, H);
   // a wave a token at most, so that no barrier is met (4096 x 1001 bf16, k = 4:
   // 16 us, a workgroup a token 26), unless each lane of a workgroup has two
-  // pieces or more (4096 x 4096 bf16, k = 2: 36.3 us, a workgroup a token 33.7)
+  // pieces or more (4096 x 4096 bf16, k = 2: 35.3 us, a workgroup a token 33.9; 1000 x
+  // 8192 fp16, k = 4: 57.5 and 28.9)
   const int sh = pieces >= 2 * kRowThreads ? 8 : lanes_log2(pieces, 6);
-  // rows in flight: 2 there (2000 x 2048 fp32, k = 8: 60.4 us, with 4 64.8), else 4
-  // for more than 2 experts (4096 x 1001: 15.7, with 2 16.6)
-  with_type(type, k <= 2 || sh == 8, [&](auto it, auto at) {
+  // rows in flight: 4 for more than 2 experts (2000 x 2048 fp32, k = 8: 63.0 us, with 2
+  // 66.4; 1000 x 8192 fp16, k = 4: 28.9 and 30.9; 4096 x 1001 bf16, k = 4: 15.7 and 16.6;
+  // against it 4096 x 4096 bf16, k = 4: 68.2 and 65.3), 2 where tokens leave half of the
+  // CUs without a workgroup: a token's places then go to more of them (1 x 8192 fp32,
+  // k = 8: 5.9 us, with 4 9.7, all places in one workgroup 18.2)
+  const unsigned blocks = token_blocks(T, sh), cus = device_cus();
+  with_type(type, k <= 2 || 2 * blocks <= cus, [&](auto it, auto at) {
+    constexpr unsigned AT = decltype(at)::value;
+    const unsigned parts = ((unsigned)k + AT - 1) / AT, room = cus / blocks;
     hipLaunchKernelGGL((k_moe_combine_grad<decltype(it)::value, decltype(at)::value>),
-                       dim3(token_blocks(T, sh) + kTailBlocks), dim3(kRowThreads), 0, stream, dy,
-                       ld, ys, offs, pos, weights, T, (int)E, (int)k, (int)H, sh, dys, dweights);
+                       dim3(blocks + kTailBlocks, parts < room ? parts : room > 1 ? room : 1),
+                       dim3(kRowThreads), 0, stream, dy, ld, ys, offs, pos, weights, T, (int)E,
+                       (int)k, (int)H, sh, dys, dweights);
   });
   return hipGetLastError();
 }

@@ -104,6 +104,35 @@ def test_combine_and_gradients(bgt, dev, T, H, E, k, kind):
     assert ((dw.double() - prod.sum(2)).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("T,H,E,k", [(1, 8192, 8, 8), (3, 4104, 16, 7), (2, 100, 32, 16),
+                                     (70, 4096, 16, 5), (300, 8192, 8, 3)])
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_combine_gradient_of_few_tokens(bgt, dev, T, H, E, k, kind):
+    """Few tokens (whose places may go to several workgroups) and the same tokens
+    among many have gradients of the same bits."""
+    say(f"combine's gradient, few tokens T={T} H={H} E={E} k={k} {kind}")
+    many = 600
+    g = torch.Generator(device=dev).manual_seed(T + H + k)
+    ids = torch.rand(many, E, generator=g, device=dev).argsort(1)[:, :k].to(torch.int32)
+    ids[torch.rand(many, k, generator=g, device=dev) < 0.1] = -1
+    rows = torch.randn(many, k, H, generator=g, device=dev).to(TYPES[kind])
+    dy = torch.randn(many, H, generator=g, device=dev).to(TYPES[kind])
+    w = torch.rand(many, k, generator=g, device=dev)
+    got = []
+    for n in (T, many):
+        offs, tok, pos = bgt.moe_sort(ids[:n].contiguous(), E)
+        ys = torch.full((n * k, H), float("nan"), dtype=TYPES[kind], device=dev)
+        there = pos >= 0
+        ys[pos[there].long()] = rows[:n][there]
+        dys, dw = bgt.moe_combine_backward(dy[:n], ys, offs, pos, w[:n])
+        assert (dys[int(offs[-1]):] == 0).all() and (dw[~there] == 0).all()
+        got.append((dys[pos[:T].clamp(min=0).long()][there[:T]], dw[:T]))
+        prod = (rows[:n].double() * dy[:n].double()[:, None]) * there[..., None]
+        tol = (H / 32 + 32) * U * prod.abs().sum(2) + 1e-37
+        assert ((dw.double() - prod.sum(2)).abs() <= tol).all()
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
 def test_combine_gradient_against_differences(bgt, dev):
     # f(ys, w) = <dy, combine(ys, w)> is linear in each: differences are exact
     # up to rounding
