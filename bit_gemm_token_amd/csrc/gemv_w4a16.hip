@@ -376,66 +376,88 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) vo
                               min(ROWS, M - r0));
 }
 
-// The j-th expert that has slots: its number, first slot and slot count; experts
-// with more than `many` slots come first. False: fewer experts have slots. Every
-// wave reads the offsets 64 experts at a time.
-__device__ __forceinline__ bool busy_expert(const Route& rt, int j, int many, int& e, int& first,
-                                            int& rows) {
+// The j-th pass over slots of one expert: the expert, the pass's first slot and slot
+// count. An expert's slots make whole passes of ROWS and one of the rest; passes of
+// more than `many` slots come before all others, and the first ones of the experts
+// before their further ones. False: there are no more. Every wave reads the offsets
+// 64 experts at a time.
+template <int ROWS>
+__device__ __forceinline__ bool find_pass(const Route& rt, int j, int many, int& e, int& first,
+                                          int& rows) {
   const int lane = threadIdx.x % kWave;
+  const bool whole_heavy = ROWS > many;
   for (int heavy = many < rt.R; heavy >= 0; --heavy)
     for (int base = 0; base < rt.E; base += kWave) {
       const int i = min(base + lane, rt.E - 1);
       const int a = clamp_route(rt.offs[i], 0, rt.R), b = clamp_route(rt.offs[i + 1], a, rt.R);
-      const bool mine = base + lane < rt.E && b > a && (b - a > many) == (heavy != 0);
-      const unsigned long long busy = __ballot(mine);
-      const int n = __popcll(busy);
-      if (j < n) {
-        const unsigned long long hit =
-            __ballot(mine && __popcll(busy & ((2ull << lane) - 1)) == j + 1);
-        const int l = __builtin_ctzll(hit);
-        e = __builtin_amdgcn_readfirstlane(base + l);
-        first = __builtin_amdgcn_readfirstlane(__shfl(a, l, kWave));
-        rows = __builtin_amdgcn_readfirstlane(__shfl(b, l, kWave)) - first;
-        return true;
+      const int n = base + lane < rt.E ? b - a : 0, whole = n / ROWS, rest = n % ROWS;
+      const int mine = (whole_heavy == (heavy != 0) ? whole : 0) +
+                       (rest > 0 && (rest > many) == (heavy != 0) ? 1 : 0);
+      const unsigned long long some = __ballot(mine > 0);
+      unsigned long long hit = 0;
+      int local = 0;
+      if (j < __popcll(some)) {
+        hit = __ballot(mine > 0 && __popcll(some & ((2ull << lane) - 1)) == j + 1);
+      } else {
+        j -= __popcll(some);
+        if (__ballot(mine > 1) == 0) continue;
+        int upto = max(mine - 1, 0);
+        for (int o = 1; o < kWave; o <<= 1) {
+          const int below = __shfl_up(upto, o, kWave);
+          if (lane >= o) upto += below;
+        }
+        const int before = upto - max(mine - 1, 0);
+        hit = __ballot(j >= before && j < upto);
+        if (hit == 0) {
+          j -= __builtin_amdgcn_readfirstlane(__shfl(upto, kWave - 1, kWave));
+          continue;
+        }
+        local = 1 + j - before;
       }
-      j -= n;
+      // the one pass of a class that whole passes are not in is the rest
+      const int pass = whole_heavy == (heavy != 0) ? local : whole;
+      const int l = __builtin_ctzll(hit);
+      e = __builtin_amdgcn_readfirstlane(base + l);
+      first = __builtin_amdgcn_readfirstlane(__shfl(a + pass * ROWS, l, kWave));
+      rows = __builtin_amdgcn_readfirstlane(__shfl(min(n - pass * ROWS, ROWS), l, kWave));
+      return true;
     }
   return false;
 }
 
-// routed: grid y counts the experts that have slots (at most one a slot, so the
-// grid of a few slots has few rows); an expert's slots go through in passes of
-// up to 4*QR / terms rows, 16 or 24 rows of A where that is enough (8 experts of
-// 14336 x 4096 with 20 slots each: 58 us as 24 rows, 62 as 32). The first y zeroes
-// the rows past the last slot.
+// routed: grid y (and z, past 65535) deals out the passes of up to 4*QR / terms rows,
+// not more than the slots can make, so the grid of a few slots has few rows. Passes
+// of one expert run side by side (8 experts of 14336 x 4096, 122 slots, calls: 61 of
+// them at two experts each 29.5 us, one after the other in a workgroup 50.2; 61 at one
+// and 8 or 9 at the others 64 to 67 and 78.7; 12 to 20 each 54 and 56). A pass takes
+// 16 or 24 rows of A where that is enough (20 slots each: 58 us as 24 rows, 62 as 32).
+// The first y zeroes the rows past the last slot.
 template <int XT, int QR, int NT, int NW>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) void k_w4a16_moe(
     const void* __restrict__ x, int64_t ldx, const uint4* __restrict__ packed,
     const float* __restrict__ fscale, int N, int G, OutY y, Route rt) {
   __shared__ __attribute__((aligned(16))) char lds[kLds<QR, NT, NW>];
-  constexpr int TERMS = kTerms<XT>;
-  if (blockIdx.y == 0) {
+  constexpr int TERMS = kTerms<XT>, ROWS = 4 * QR / TERMS;
+  if (blockIdx.y == 0 && blockIdx.z == 0) {
     const int c0 = 16 * NT * blockIdx.x, cols = min(16 * NT, N - c0);
     const int last = clamp_route(rt.offs[rt.E], 0, rt.R);
     for (int64_t o = threadIdx.x; o < (int64_t)(rt.R - last) * cols; o += NW * 64)
       y.put((last + o / cols) * N + c0 + o % cols, 0.0f);
   }
-  int e, first, rows;
   // with blocks of 16 rows and larger ones in a launch the larger start first, so
   // that a CU's workgroups are of both kinds (8 experts of 14336 x 4096, 61
   // tokens: 57.1 -> 55.0 us)
-  if (!busy_expert(rt, blockIdx.y, QR > 4 ? 16 / TERMS : rt.R, e, first, rows)) return;
+  const int many = QR > 4 ? 16 / TERMS : rt.R;
+  int e, first, nr;
+  if (!find_pass<ROWS>(rt, blockIdx.z * gridDim.y + blockIdx.y, many, e, first, nr)) return;
   packed += (int64_t)e * rt.wstride / 16;
   fscale += (int64_t)e * rt.sstride;
-  for (int r0 = 0, nr = 0; r0 < rows; r0 += nr) {
-    nr = min(rows - r0, 4 * QR / TERMS);
-    if (QR > 4 && nr * TERMS <= 16)
-      run_rows<XT, 4, NT, NW>(lds, x, ldx, packed, fscale, N, G, y, rt, true, first + r0, nr);
-    else if (QR > 6 && nr * TERMS <= 24)
-      run_rows<XT, 6, NT, NW>(lds, x, ldx, packed, fscale, N, G, y, rt, true, first + r0, nr);
-    else
-      run_rows<XT, QR, NT, NW>(lds, x, ldx, packed, fscale, N, G, y, rt, true, first + r0, nr);
-  }
+  if (QR > 4 && nr * TERMS <= 16)
+    run_rows<XT, 4, NT, NW>(lds, x, ldx, packed, fscale, N, G, y, rt, true, first, nr);
+  else if (QR > 6 && nr * TERMS <= 24)
+    run_rows<XT, 6, NT, NW>(lds, x, ldx, packed, fscale, N, G, y, rt, true, first, nr);
+  else
+    run_rows<XT, QR, NT, NW>(lds, x, ldx, packed, fscale, N, G, y, rt, true, first, nr);
 }
 
 template <int XT, int QR, int NT, int NW>
@@ -450,8 +472,11 @@ static void launch_dense(const void* x, int64_t ldx, const uint8_t* packed, cons
 template <int XT, int QR, int NT, int NW>
 static void launch_routed(const void* x, int64_t ldx, const uint8_t* packed, const float* fscale,
                           int N, int K, OutY y, const Route& rt, hipStream_t stream) {
-  const int tiles = N / 16;
-  hipLaunchKernelGGL((k_w4a16_moe<XT, QR, NT, NW>), dim3((tiles + NT - 1) / NT, min(rt.E, rt.R)),
+  // the most passes that R slots of E experts make
+  const int tiles = N / 16, busy = min(rt.E, rt.R);
+  const int passes = busy + (rt.R - busy) / (4 * QR / kTerms<XT>);
+  const int ny = min(passes, 65535), nz = (passes + ny - 1) / ny;
+  hipLaunchKernelGGL((k_w4a16_moe<XT, QR, NT, NW>), dim3((tiles + NT - 1) / NT, ny, nz),
                      dim3(NW * 64), 0, stream, x, ldx, reinterpret_cast<const uint4*>(packed),
                      fscale, N, K / kGroup, y, rt);
 }
@@ -518,7 +543,7 @@ template <int XT>
 static void routed_of_type(const void* x, int64_t ldx, const uint8_t* packed, const float* fscale,
                            int N, int K, OutY y, const Route& rt, hipStream_t stream) {
   // rows an expert gets at most, and half as many again as the mean: an expert
-  // with more takes another pass over its (cached) weights
+  // with more takes another pass over its (cached) weights, in other workgroups
   const int busy = min(rt.E, rt.R);
   const int rows = min(min(rt.T, rt.R), (3 * rt.R / rt.E + 1) / 2 + 1);
   with_shape<XT>(rows * kTerms<XT>, busy * (N / 16), K / kGroup, [&](auto qr, auto nt, auto nw) {

@@ -229,6 +229,17 @@ def test_routed_dropped_and_skewed(bgt, dev, kind):
     check_moe(bgt, dev, slots(12, 8, 2, 4), 8, 640, 144, dt, 4, out=torch.float32)
 
 
+@pytest.mark.parametrize("counts", [[33, 1, 16, 17, 0, 24, 25, 6], [61, 9, 9, 9, 9, 9, 8, 8], [32] * 4,
+                                    [0, 65, 0, 64, 1], [200, 0, 1, 130], [0] * 70 + [40] + [1] * 30 + [90, 0, 35]])
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_experts_of_several_passes(bgt, dev, counts, kind):
+    """Experts with more slots than one pass takes, next to ones with few or none."""
+    say(f"moe gemv counts={counts} {kind}")
+    ids = np.repeat(np.arange(len(counts), dtype=np.int32), counts)[:, None]
+    np.random.default_rng(len(ids)).shuffle(ids)
+    check_moe(bgt, dev, ids, len(counts), 256, 48, TYPES[kind], len(ids))
+
+
 def test_routing_that_points_outside(bgt, dev):
     # offsets and tokens are clamped: nothing outside the buffers is touched
     T, E, K, N, R = 4, 3, 256, 32, 8
