@@ -375,8 +375,10 @@ __global__ __launch_bounds__(256) void k_route_grad(const float* __restrict__ dw
   const bool in = t < T;
   const int n = (int)min((int64_t)TOKENS, T - tr) * k;
   for (int o = threadIdx.x; o < n; o += 256) {
+    // an id past E may fall on a lane's padding, where 0 * dweight would meet the sum
+    const int id = ids[tr * k + o];
     sdw[o] = dw[tr * k + o];
-    sid[o] = ids[tr * k + o];
+    sid[o] = id >= 0 && id < E ? id : -1;
   }
   float v[V], d[V];
   if (in) {
