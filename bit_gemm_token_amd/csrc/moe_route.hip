@@ -389,7 +389,7 @@ __global__ __launch_bounds__(256) void k_route_grad(const float* __restrict__ dw
     for (int j = 0; j < V; ++j) v[j] = kNegInf;
   }
   __syncthreads();
-  unsigned hit = 0;
+  unsigned hit = all ? ~0u : 0;                    // logits that the softmax is over
 #pragma unroll
   for (int j = 0; j < V; ++j) d[j] = 0.0f;
   if (in)
@@ -406,7 +406,7 @@ __global__ __launch_bounds__(256) void k_route_grad(const float* __restrict__ dw
   float m = kNegInf;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    if (!all && !(hit >> j & 1)) v[j] = kNegInf;
+    if (!(hit >> j & 1)) v[j] = kNegInf;
     m = fmaxf(m, v[j]);
   }
   m = lanes_max<L>(m);
@@ -425,8 +425,9 @@ __global__ __launch_bounds__(256) void k_route_grad(const float* __restrict__ dw
     dot = __builtin_fmaf(v[j], d[j], dot);
   }
   dot = lanes_sum<L>(dot);
+  // the others' gradient is 0, also where the sum is not finite
 #pragma unroll
-  for (int j = 0; j < V; ++j) v[j] *= d[j] - dot;
+  for (int j = 0; j < V; ++j) v[j] = hit >> j & 1 ? v[j] * (d[j] - dot) : 0.0f;
   const OutY out{dl, IT};
   const int64_t o = t * E + V * l;
   constexpr int W = IT == kF32 ? 4 : 8;

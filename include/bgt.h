@@ -463,9 +463,13 @@ int64_t bgt_moe_sort_workspace_bytes(int64_t T, int64_t E, int64_t k);
 /* bgt_moe_route_backward -- gradient of the logits from that of the weights:
  *     dl_tj = p_tj (d_tj - sum_n p_tn d_tn),
  * d_tj = dweights[t][i] for the expert j = ids[t][i] and 0 for the others, p
- * the softmax over the chosen experts (0 elsewhere) or over all (norm as in
- * the forward call). Places with ids outside [0, E) have no gradient; a token
- * with nothing to normalise over gets zeros. dlogits: T x E of `type`, dense. */
+ * the softmax over the chosen experts or over all (norm as in the forward
+ * call). Under BGT_NORM_CHOSEN the experts not chosen get 0, also where a
+ * chosen logit or a dweight that is not finite makes the chosen ones' gradient
+ * so; under BGT_NORM_ALL such values reach all of the token's experts, as in
+ * the formula. Places with ids outside [0, E) have no gradient, whatever
+ * dweights holds there; a token with nothing to normalise over gets zeros.
+ * dlogits: T x E of `type`, dense. */
 int bgt_moe_route_backward(const float* dweights, const void* logits, int type, int64_t ld,
                            const int32_t* ids, int64_t T, int64_t E, int64_t k, int norm,
                            void* dlogits, void* stream);

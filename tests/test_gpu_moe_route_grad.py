@@ -1,7 +1,8 @@
 """The routing gradient where ids or values are not ordinary ones.
 
 Places whose id is outside [0, E) have no gradient, whatever their dweights hold and
-wherever the id falls (a token's lanes cover up to twice E experts).
+wherever the id falls (a token's lanes cover up to twice E experts). With norm "chosen"
+the experts not chosen have a gradient of zero, whatever the others' is.
 """
 import numpy as np
 import pytest
@@ -79,3 +80,48 @@ def test_ids_outside(bgt, dev, E, norm):
         # the inner sum over a tree of depth at most 12, two more operations
         tol = size * 160 * U + np.abs(want) * HALF_ULP[kind] + (6e-8 if kind == "f16" else 1e-37)
         assert (np.abs(got.cpu().double().numpy() - want) <= tol).all()
+
+
+@pytest.mark.parametrize("E,k", [(2, 1), (8, 2), (9, 4), (60, 6), (130, 16)])
+def test_values_that_are_not_finite(bgt, dev, E, k):
+    """Norm "chosen": the weights do not depend on the experts not chosen, whose gradient
+    is zero whatever the chosen ones' is, and tokens do not reach each other."""
+    g = np.random.default_rng(E + k)
+    T = 40
+    ids = distinct(g, T, E, k)
+    ids[3, 1:] = -1
+    v = g.standard_normal((T, E)).astype(np.float32)
+    dw = g.standard_normal((T, k)).astype(np.float32)
+    plain = dw.copy(), v.copy()
+    odd = np.array([2, 3, 5, 7, 11, 13, 17, 39])
+    dw[2, 0], dw[3, 0], dw[5, k - 1], dw[7] = np.inf, np.nan, -np.inf, np.nan
+    dw[39, 0], dw[39, k - 1] = -np.inf, np.inf
+    v[11, ids[11, 0]] = np.inf                     # chosen
+    v[13, ids[13]] = np.inf
+    v[17, ids[17, k - 1]] = np.nan
+    others = np.ones((T, E + 1), bool)
+    np.put_along_axis(others, np.where(ids >= 0, ids, E), False, 1)
+    others = others[:, :E]
+    v[others & (g.random((T, E)) < 0.2)] = np.inf  # not chosen: of no account
+    v[others & (g.random((T, E)) < 0.2)] = np.nan
+    fine = np.setdiff1d(np.arange(T), odd)
+    for kind, dt in TYPES.items():
+        print(f"routing gradient, values not finite, E={E} k={k} {kind}", flush=True)
+
+        def call(d, l):
+            return bgt.moe_route_backward(torch.from_numpy(d).to(dev), torch.from_numpy(l).to(dt).to(dev),
+                                          torch.from_numpy(ids).to(dev)).cpu().double().numpy()
+
+        got = call(dw, v)
+        assert (got[others] == 0).all()
+        assert np.array_equal(got[fine], call(*plain)[fine])
+        # of the chosen ones the formula's: NaN where it has inf - inf, 0 * inf or NaN
+        lw = np.where(others, 0.0, torch.from_numpy(v).to(dt).double().numpy())
+        for t in odd:
+            at = ids[t][ids[t] >= 0]
+            with np.errstate(invalid="ignore"):
+                e = np.exp(lw[t, at] - lw[t, at].max())
+                p, d = e / e.sum(), dw[t, :len(at)].astype(np.float64)
+                want = p * (d - (p * d).sum())
+            assert np.array_equal(np.isnan(got[t, at]), np.isnan(want))
+            assert np.array_equal(got[t, at][np.isinf(want)], want[np.isinf(want)])
