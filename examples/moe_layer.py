@@ -16,6 +16,7 @@ import sys
 import time
 
 import torch
+from torch.autograd.function import once_differentiable
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import bit_gemm_token_amd as bgt  # noqa: E402
@@ -54,6 +55,7 @@ class ServedExperts:
 
 
 # ----------------------------------------------------------------------- training
+# The library's backward calls leave no graph: a second derivative is refused.
 class Route(torch.autograd.Function):
     """logits -> (weights, ids, offs, tok, pos)"""
 
@@ -65,6 +67,7 @@ class Route(torch.autograd.Function):
         return weights, ids, offs, tok, pos
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dweights, *_):
         logits, ids = ctx.saved_tensors
         return bgt.moe_route_backward(dweights.contiguous(), logits, ids), None
@@ -77,6 +80,7 @@ class Gather(torch.autograd.Function):
         return bgt.moe_gather(x, offs, pos)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dxs):
         return bgt.moe_gather_backward(dxs.contiguous(), ctx.saved_tensors[0]), None, None
 
@@ -88,6 +92,7 @@ class Combine(torch.autograd.Function):
         return bgt.moe_combine(ys, pos, weights)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         ys, offs, pos, weights = ctx.saved_tensors
         dys, dweights = bgt.moe_combine_backward(dy.contiguous(), ys, offs, pos, weights)
