@@ -10,10 +10,11 @@
 // -inf and NaN logits are never chosen; a token with fewer than k others has
 // expert -1 and weight 0 in its last places, and those slots are dropped.
 //
-// The work is a few bytes a token, so launches and round trips bound it: up to
-// kSingleSlots slots one workgroup chooses and sorts in one launch; beyond, the
-// choosing launch also leaves each workgroup's slot counts by expert, and a
-// second launch sorts, every workgroup adding up the counts before its own.
+// The work is a few bytes a token, so launches and round trips bound it: few
+// tokens (one_launch) are chosen for and sorted by one workgroup in one launch;
+// otherwise the choosing launch also leaves each workgroup's slot counts by
+// expert, and a second launch sorts, every workgroup adding up the counts before
+// its own.
 // Kernel times: one token of 8 experts 3.6 us, 4096 tokens of 8 experts, k = 2, 8.8
 // us (3.8 to choose, 5.0 to sort), 16381 tokens of 64 experts, k = 6, 12.7 us (6.6 and
 // 6.1) and 5.2 us for the gradient.
@@ -25,7 +26,7 @@ namespace bgt {
 constexpr int kMaxE = 256;          // experts
 constexpr int kMaxK = 16;           // experts of a token
 constexpr int kMaxChunks = 256;     // workgroups a sort is split into
-constexpr int64_t kSingleSlots = 1024;
+constexpr int64_t kSingleSlots = 1024;  // slots one workgroup sorts
 constexpr float kNegInf = -__builtin_inff();
 
 // ------------------------------------------------------------- counting sort
@@ -281,8 +282,8 @@ __device__ __forceinline__ void lanes_best(float& best, int& at) {
 }
 
 // --------------------------------------------------------------------- top k
-// waves of a workgroup: up to 128 tokens at once with 4 lanes a token or fewer,
-// 32 to 64 with more
+// waves of a workgroup: 128 or 64 tokens at once with 2 or 4 lanes a token, 64, 32
+// or 16 with 8, 16 or 32
 template <int L> constexpr int kTopWaves = L <= 4 ? 4 : 8;
 
 // Workgroup b chooses for tokens [b*tb, (b+1)*tb) and leaves its slots' counts
@@ -472,6 +473,18 @@ int tokens_at_once(int E) {
   return n;
 }
 
+// whether one workgroup chooses and sorts in one launch. Its rounds of tokens
+// follow each other, about 0.75 + 0.5 k us each; two launches cost the host 2.6 us
+// more and the device about 2. Kernels, one launch / two, us: 256 tokens of 8
+// experts, k = 2 (2 rounds) 5.6 / 6.6, 512 (4 rounds) 8.8 / 6.7; 64 of 128, k = 8 (2
+// rounds) 11.5 / 9.8, 128 (4) 20.5 / 10.0; 1024 of 8, k = 1 (8) 10.7 / 6.6; 1024 of
+// 256, k = 1 (64) 85 / 8.3. Calls that are waited for: 25.3 / 27.6, 28.1 / 27.6; 30.5 /
+// 29.4, 39.6 / 29.4; 30.1 / 28.6; 104 / 28.
+bool one_launch(int64_t T, int64_t E, int64_t k) {
+  const int64_t round = tokens_at_once((int)E), rounds = (T + round - 1) / round;
+  return T * k <= kSingleSlots && (rounds - 1) * (3 + 2 * k) <= 21;
+}
+
 // tokens of a workgroup where several sort: one round of the choosing kernel,
 // more where that would take over kMaxChunks workgroups
 int64_t chunk_tokens(int64_t T, int64_t E) {
@@ -510,9 +523,10 @@ void launch_place(const int32_t* ids, int64_t R, int64_t chunk, int E, int k, co
 
 }  // namespace
 
-// the chunks' counts; one workgroup needs none
+// the chunks' counts; one workgroup needs none. (Where one_launch holds the sort
+// alone is one launch too, so this is enough for both.)
 int64_t moe_sort_ws_bytes(int64_t T, int64_t E, int64_t k) {
-  if (T * k <= kSingleSlots) return 0;
+  if (one_launch(T, E, k)) return 0;
   const int64_t tb = chunk_tokens(T, E);
   return (T + tb - 1) / tb * E * 4;
 }
@@ -535,7 +549,7 @@ hipError_t launch_moe_sort(const int32_t* ids, int64_t T, int64_t E, int64_t k, 
 hipError_t launch_moe_route(const void* logits, int type, int64_t ld, int64_t T, int64_t E,
                             int64_t k, bool all, float* weights, int32_t* ids, int32_t* offs,
                             int32_t* tok, int32_t* pos, int32_t* ws, hipStream_t stream) {
-  const bool single = T * k <= kSingleSlots;
+  const bool single = one_launch(T, E, k);
   const int64_t tb = single ? T : chunk_tokens(T, E);
   int32_t* counts = single ? nullptr : ws;
   const int e = (int)E, n = (int)k;
