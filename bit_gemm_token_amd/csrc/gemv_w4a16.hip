@@ -480,7 +480,7 @@ static void launch_routed(const void* x, int64_t ldx, const uint8_t* packed, con
                      dim3(NW * 64), 0, stream, x, ldx, reinterpret_cast<const uint4*>(packed),
                      fscale, N, K / kGroup, y, rt);
 }
-#ifndef BGT_GEMV_SWEEP
+
 // Column tiles a workgroup of more than one row quad takes, for `tiles` tiles in
 // the whole launch (more than one a CU): what the busiest CU then has to do,
 // each workgroup's rows counted as 0.3 tiles a quad. Sweeps (us), 1 / 2 / 3 / 4
@@ -572,6 +572,5 @@ hipError_t launch_w4a16_moe(const void* x, int x_type, int64_t ldx, int64_t T, c
   else routed_of_type<kBF16>(x, ldx, packed, fscale, n, k, y, rt, stream);
   return hipGetLastError();
 }
-#endif
 
 }  // namespace bgt
