@@ -18,9 +18,12 @@
 // i becomes rows 3i, 3i+1, 3i+2 of A, whose products are added at the end.
 //
 // The weights' bytes bound it where they are many: 2 experts of 4096 x 14336, one
-// token, 13 us (62 MB); 16 x 4096 x 22016 fp16 11.3 us (48 MB). Small products are
+// token, 13.0 us (62 MB); 16 x 4096 x 22016 fp16 11.3 us (49 MB). Small products are
 // bound by a launch and its round trips (1 x 4096 x 4096 4.1 us), few fp32 rows
-// also by splitting them (3 x 11008 x 4096 10.0 us).
+// also by splitting them (3 x 11008 x 4096 10.2 us), and 17 to 64 rows by the rows:
+// every workgroup reads all of them for its 16 to 64 columns, and more than 32 take
+// the weights twice (4096 x 22016 fp16, 32 and 64 rows 15.6 and 29.3 us; 64 x 14336 x
+// 4096 19.3).
 #include <type_traits>
 
 #include "device_common.h"
@@ -429,7 +432,10 @@ __device__ __forceinline__ bool find_pass(const Route& rt, int j, int many, int&
 // not more than the slots can make, so the grid of a few slots has few rows. Passes
 // of one expert run side by side (8 experts of 14336 x 4096, 122 slots, calls: 61 of
 // them at two experts each 29.5 us, one after the other in a workgroup 50.2; 61 at one
-// and 8 or 9 at the others 64 to 67 and 78.7; 12 to 20 each 54 and 56). A pass takes
+// and 8 or 9 at the others 64 to 67 and 78.7; 12 to 20 each 54 and 56). The further
+// passes find the weights in the Infinity Cache only where those of all busy experts
+// fit it: of 64 experts of 14336 x 4096, 1.9 GB and 512 slots, 8 each 350 us, 20 at 16
+// of them and 4 at the others 418 (351 as one pass each of up to 32 rows). A pass takes
 // 16 or 24 rows of A where that is enough (20 slots each: 58 us as 24 rows, 62 as 32).
 // The first y zeroes the rows past the last slot.
 template <int XT, int QR, int NT, int NW>
@@ -483,10 +489,15 @@ static void launch_routed(const void* x, int64_t ldx, const uint8_t* packed, con
 
 // Column tiles a workgroup of more than one row quad takes, for `tiles` tiles in
 // the whole launch (more than one a CU): what the busiest CU then has to do,
-// each workgroup's rows counted as 0.3 tiles a quad. Sweeps (us), 1 / 2 / 3 / 4
-// tiles a workgroup: 16 x 4096 x 22016 fp16 (1376 tiles) 13.7 / 13.2 / 11.3 /
-// 12.8; 32 x 4096 x 22016 bf16 22.6 / 17.2 / 17.0 / 24.2; 8 experts of 14336 x
-// 4096, 61 tokens fp16 (2048 tiles) - / 73.8 / 72.1 / 65.4.
+// each workgroup's rows counted as 0.3 tiles a quad. Sweeps (us), 2 / 3 / 4 tiles a
+// workgroup, [taken]: 16 x 4096 fp16 at N = 8192 [6.9] / 7.1 / 8.0, 11008 8.1 / [7.5] /
+// 8.1, 14336 9.0 / 10.2 / [8.7], 22016 13.0 / [11.7] / 14.2, 28672 17.5 / 15.7 / [13.8];
+// 32 x 14336 fp16 at 8192 [19.7] / 24.9 / 26.2, 11008 37 / [25] / 30, 14336 43 / 48 /
+// [37]; 8 experts of 14336 x 4096, 61 tokens 73.8 / 72.1 / [65.4]. It does not know that
+// four tiles of 32 rows of 16 bits need more registers than there are (256, 25 to
+// 34 of them spilled), which costs where K is short: 32 x 4096 fp16 at N =
+// 14336 11.3 / 14.1 / [13.3], 22016 16.1 / [16.0] / 22.6, 28672 20.1 / 21.9 / [22.0], 32768
+// 21.0 / 24.0 / [25.6]; 48 rows at 22016 28.3 / 26.2 / [29.5].
 static int tiles_per_wg(int tiles, int qr) {
   const int cus = device_cus();
   int best = 2;
@@ -504,9 +515,14 @@ static int tiles_per_wg(int tiles, int qr) {
 // have the splitting to do: 3 x 11008 x 4096 10.7 -> 9.6 us). More: 4 waves, for
 // up to 4 rows of A, whose rows cost little, with one tile (1 x 4096 x 11008
 // bf16, 1 / 2 / 3 / 4 tiles: 6.2 / 7.9 / 7.3 / 8.7 us; 2 experts of 4096 x 14336,
-// one token: 12.5 / 13.9 / 14.1 / 14.2), in launches that stream 192 MiB and
-// more four (14336 x 32768: 61 with one, 47 with four; 14336 x 28672: 45 and 43;
-// below, 14336 x 22016: 35 and 38); for more rows as tiles_per_wg says.
+// one token: 12.5 / 13.9 / 14.1 / 14.2), in launches of 192 MiB of weights and more
+// with four: no mechanism is known, only the sweeps. One / four tiles, one row of
+// bf16, one of fp16, four of fp16, one of fp32: 14336 x 22016 (150 MiB) 35 / 39, 34 / 36,
+// 35 / 37, 41 / 44; 28672 (196 MiB) 44 / 44, 43 / 43, 47 / 43, 46 / 48; 32768 (224 MiB)
+// 51 / 50, 58 / 49, 57 / 50, 53 / 50; 57344 (392 MiB) 85 / 96, 82 / 92, 91 / 90, 91 / 90;
+// 4096 x 98304 (192 MiB) 43 / 43, 40 / 42, 42 / 41, 45 / 44; routed, one token of bf16, 6
+// and 8 experts of 4096 x 14336 (168 and 224 MiB) 40 / 40 and 53 / 49. For more rows as
+// tiles_per_wg says.
 template <int XT, typename F>
 static void with_shape(int rows, int tiles, int groups, F f) {
   constexpr int FEW = XT == kF32 ? 16 : 8;
@@ -543,7 +559,7 @@ template <int XT>
 static void routed_of_type(const void* x, int64_t ldx, const uint8_t* packed, const float* fscale,
                            int N, int K, OutY y, const Route& rt, hipStream_t stream) {
   // rows an expert gets at most, and half as many again as the mean: an expert
-  // with more takes another pass over its (cached) weights, in other workgroups
+  // with more takes another pass over its weights, in other workgroups
   const int busy = min(rt.E, rt.R);
   const int rows = min(min(rt.T, rt.R), (3 * rt.R / rt.E + 1) / 2 + 1);
   with_shape<XT>(rows * kTerms<XT>, busy * (N / 16), K / kGroup, [&](auto qr, auto nt, auto nw) {

@@ -15,9 +15,10 @@
 // otherwise the choosing launch also leaves each workgroup's slot counts by
 // expert, and a second launch sorts, every workgroup adding up the counts before
 // its own.
-// Kernel times: one token of 8 experts 3.6 us, 4096 tokens of 8 experts, k = 2, 8.8
-// us (3.8 to choose, 5.0 to sort), 16381 tokens of 64 experts, k = 6, 12.7 us (6.6 and
-// 6.1) and 5.2 us for the gradient.
+// Kernel times: one token of 8 experts 3.6 us, 64 tokens of 256 experts, k = 8, 11.0 us
+// (6.7 to choose, 4.3 to sort), 4096 tokens of 8 experts, k = 2, 8.9 us (3.8 and 5.1),
+// 16381 tokens of 64 experts, k = 6, 12.6 us (6.7 and 5.9) and 5.3 us for the gradient;
+// the sort alone of the last two 7.3 us (2.3 to count, 5.0 to place) and 8.9 (2.8, 6.1).
 #include "device_common.h"
 #include "launch.h"
 

@@ -152,9 +152,10 @@ __global__ __launch_bounds__(kRowThreads) void k_moe_gather(const T* __restrict_
 
 // AT: expert rows of a token in flight together. A dropped place reads row 0 and
 // uses none of it, which costs less than a branch around the load. All three
-// kernels run near the rate of a copy (5.2 TB/s): 4096 x 4096 bf16, k = 2, gather
-// 16.2 us (100 MB, partly from the Infinity Cache), combine's gradient 33.4 us (168
-// MB).
+// kernels run near the rate of a copy (5.2 TB/s) where the rows are many: 4096 x 4096
+// bf16, k = 2, gather 16.1 us, combine 16.2 (100 MB each, partly from the Infinity
+// Cache), combine's gradient 31.2 (168 MB). Smaller ones are bound by launch and
+// ramp (8192 x 127 fp16, k = 4, 10 MB, combine 5.4 us).
 template <int IT, int AT>
 __global__ __launch_bounds__(kRowThreads) void k_moe_combine(const void* __restrict__ ys,
                                                              const int32_t* __restrict__ pos,
@@ -327,7 +328,8 @@ hipError_t launch_moe_combine(const void* ys, int type, const int32_t* pos, cons
   const unsigned blocks = token_blocks(T, sh);
   with_type(type, k <= 2, [&](auto it, auto at) {
     hipLaunchKernelGGL((k_moe_combine<decltype(it)::value, decltype(at)::value>),
-                       dim3(blocks, row_blocks(pieces, blocks)), dim3(kRowThreads), 0, stream, ys, pos, weights, T, (int)k, (int)H, sh, y);
+                       dim3(blocks, row_blocks(pieces, blocks)), dim3(kRowThreads), 0, stream, ys,
+                       pos, weights, T, (int)k, (int)H, sh, y);
   });
   return hipGetLastError();
 }
