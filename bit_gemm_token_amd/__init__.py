@@ -34,6 +34,21 @@ Mixture-of-experts routing and rows, and weight-only products of few rows:
     moe_combine_backward(dy, ys, offs, pos, weights) -> (dys, dweights)
     w4a16_gemv(x, packed, fscale, N)       -> y
     w4a16_moe_gemv(x, offs, tok, packed, fscale, N)  -> y
+
+8-bit floating-point rows and weights (torch.float8_e4m3fn codes, torch.float8_e8m0fnu scales of
+128 elements), their products, the weights' gradients, and a router's balance loss:
+    quantize_fp8(x)                        -> (q, scale)
+    dequantize_fp8(q, scale, K, out_dtype) -> x
+    pack_weights_fp8(w, turned=False)      -> dict(qw, sw[, qt, st])
+    w8a8_gemm_fp8(qx, sx, qw, sw)          -> y
+    w8a8_linear_fp8(x, qw, sw)             -> (y, qx, sx)
+    w8a8_moe_gemm_fp8(qx, sx, offs, tok, qw, sw)     -> y
+    wgrad_fp8(qx, sx, dy, K)               -> dw
+    moe_wgrad_fp8(qx, sx, offs, tok, dy, K)          -> dw
+    silu_mul_fp8(gate, up)                 -> (hq, hs, gq, gs, uq, us)
+    silu_mul_fp8_backward(dh, gq, gs, uq, us)        -> (dgate, dup)
+    moe_balance(logits, ids)               -> (loss, counts, probs, tokens)
+    moe_balance_backward(dloss, logits, counts, tokens) -> dlogits
 """
 from __future__ import annotations
 
@@ -70,6 +85,11 @@ EXPORTED = (
     "bgt_moe_route", "bgt_moe_sort", "bgt_moe_sort_workspace_bytes", "bgt_moe_route_backward",
     "bgt_moe_gather", "bgt_moe_combine", "bgt_moe_combine_backward", "bgt_w4a16_gemv",
     "bgt_w4a16_moe_gemv",
+    "bgt_quantize_fp8", "bgt_dequantize_fp8", "bgt_pack_weights_fp8", "bgt_w8a8_gemm_fp8",
+    "bgt_w8a8_linear_fp8", "bgt_w8a8_moe_gemm_fp8", "bgt_wgrad_fp8",
+    "bgt_wgrad_fp8_workspace_bytes", "bgt_moe_wgrad_fp8", "bgt_silu_mul_fp8",
+    "bgt_silu_mul_fp8_backward", "bgt_moe_balance", "bgt_moe_balance_workspace_bytes",
+    "bgt_moe_balance_backward",
 )
 _NAMES = ("bgt_status_string", "bgt_w4a8_kernel_name", "bgt_w8a8_is_kernel_name",
           "bgt_w4a8_moe_kernel_name")
@@ -127,10 +147,26 @@ def lib():
         L.bgt_moe_combine_backward.argtypes = [P, I64, P, I, P, P, P, I64, I64, I64, I64, P, P, P]
         L.bgt_w4a16_gemv.argtypes = [P, I, I64, P, P, I64, I64, I64, P, I, P]
         L.bgt_w4a16_moe_gemv.argtypes = [P, I, I64, I64, P, P, I64, I64, P, P, I64, I64, P, I, P]
+        L.bgt_quantize_fp8.argtypes = [P, I, I64, I64, I64, P, P, P]
+        L.bgt_dequantize_fp8.argtypes = [P, P, I64, I64, P, I, P]
+        L.bgt_pack_weights_fp8.argtypes = [P, I, I64, I64, I64, P, P, P, P, P]
+        L.bgt_w8a8_gemm_fp8.argtypes = [P, P, P, P, I64, I64, I64, P, I, P]
+        L.bgt_w8a8_linear_fp8.argtypes = [P, I, I64, P, P, I64, I64, I64, P, P, P, I, P]
+        L.bgt_w8a8_moe_gemm_fp8.argtypes = [P, P, I64, P, P, I64, I64, P, P, I64, I64, P, I, P]
+        L.bgt_wgrad_fp8.argtypes = [P, P, P, I, I64, I64, I64, I64, P, P, I64, P]
+        L.bgt_wgrad_fp8_workspace_bytes.argtypes = [I64, I64, I64]
+        L.bgt_moe_wgrad_fp8.argtypes = [P, P, I64, P, P, I64, I64, P, I, I64, I64, I64, P, P]
+        L.bgt_silu_mul_fp8.argtypes = [P, I64, P, I64, I, I64, I64, P, P, P, P, P, P, P]
+        L.bgt_silu_mul_fp8_backward.argtypes = [P, I, I64, P, P, P, P, I64, I64, P, P, P]
+        L.bgt_moe_balance.argtypes = [P, I, I64, P, I64, I64, I64, P, P, P, P, P, I64, P]
+        L.bgt_moe_balance_workspace_bytes.argtypes = [I64, I64]
+        L.bgt_moe_balance_backward.argtypes = [P, P, I, I64, P, P, I64, I64, P, P]
         for f in EXPORTED:
             getattr(L, f).restype = ctypes.c_char_p if f in _NAMES else I
         L.bgt_w4a8_workspace_bytes.restype = I64
         L.bgt_moe_sort_workspace_bytes.restype = I64
+        L.bgt_wgrad_fp8_workspace_bytes.restype = I64
+        L.bgt_moe_balance_workspace_bytes.restype = I64
         _lib = L
     return _lib
 
@@ -755,3 +791,285 @@ def w4a16_moe_gemv(x, offsets, slot_token, packed, fscale, N: int, y=None, out_d
                                   _stream(x.device))
     _raise("bgt_w4a16_moe_gemv", st)
     return y
+
+
+# ------------------------------------------------- 8-bit floating-point rows and weights
+def _padded(n):
+    return -(-n // GROUP) * GROUP
+
+
+def _on(dev, **tensors):
+    """All tensors on the device dev."""
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+
+
+def _call(fn, dev, *args):
+    """The entry point on the device's current stream, with the device made current."""
+    torch = _torch()
+    if dev.index != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            st = getattr(lib(), fn)(*args, _stream(dev))
+    else:
+        st = getattr(lib(), fn)(*args, _stream(dev))
+    _raise(fn, st)
+
+
+def _check_rows8(q, scale, name, rows=None, cols=None):
+    """(rows, padded columns) of codes M x K' and scales K'/128 x M."""
+    torch = _torch()
+    _check(q, name, torch.float8_e4m3fn)
+    if q.dim() != 2 or q.shape[1] % GROUP != 0:
+        raise ValueError(f"{name} must be rows x a multiple of {GROUP}")
+    M, Kp = q.shape
+    if rows is not None and (M, Kp) != (rows, cols):
+        raise ValueError(f"{name} must have shape {(rows, cols)}, got {(M, Kp)}")
+    _check(scale, "scale of " + name, torch.float8_e8m0fnu, (Kp // GROUP, M))
+    _on(q.device, **{"scale of " + name: scale})
+    return M, Kp
+
+
+def _check_weights8(qw, sw, Kp, E=None):
+    """N of codes (E x) N x K' and scales (E x) K'/128 x N'/128."""
+    torch = _torch()
+    _check(qw, "qw", torch.float8_e4m3fn)
+    lead = () if E is None else (E,)
+    if qw.dim() != len(lead) + 2 or tuple(qw.shape[:-2]) != lead or qw.shape[-1] != Kp:
+        raise ValueError(f"qw must be {'E x ' if E is not None else ''}N x {Kp}, got {tuple(qw.shape)}")
+    N = qw.shape[-2]
+    _check(sw, "sw", torch.float8_e8m0fnu, (*lead, Kp // GROUP, _padded(N) // GROUP))
+    return N
+
+
+def _logical(K, Kp):
+    """K columns of which the codes hold Kp (K None: all of them)."""
+    K = Kp if K is None else int(K)
+    if K < 1 or _padded(K) != Kp:
+        raise ValueError(f"K must be at most {Kp} and above {Kp - GROUP}, got {K}")
+    return K
+
+
+def quantize_fp8(x, q=None, scale=None):
+    """Rows (M x K float32, float16 or bfloat16) as 8-bit floating-point codes with a power of
+    two for each block of 128: q (M x K' float8_e4m3fn, K' the next multiple of 128, zeros
+    behind K) and scale (K'/128 x M float8_e8m0fnu). Their values are what an activation
+    checkpoint keeps: see w8a8_gemm_fp8, wgrad_fp8 and dequantize_fp8."""
+    torch = _torch()
+    M, K, ld = _rows(x, "x")
+    xt, dev, Kp = _elem_type(x, "x"), x.device, _padded(K)
+    q = _out(q, "q", torch.float8_e4m3fn, (M, Kp), dev)
+    scale = _out(scale, "scale", torch.float8_e8m0fnu, (Kp // GROUP, M), dev)
+    _on(dev, q=q, scale=scale)
+    _call("bgt_quantize_fp8", dev, _ptr(x), xt, M, K, ld, _ptr(q), _ptr(scale))
+    return q, scale
+
+
+def dequantize_fp8(q, scale, K=None, y=None, out_dtype=None):
+    """The values of quantize_fp8's codes, M x K (K None: the padded size), in y's dtype, else
+    out_dtype, else float32."""
+    torch = _torch()
+    M, Kp = _check_rows8(q, scale, "q")
+    K = _logical(K, Kp)
+    y = _out(y, "y", (out_dtype or torch.float32) if y is None else y.dtype, (M, K), q.device)
+    _on(q.device, y=y)
+    _call("bgt_dequantize_fp8", q.device, _ptr(q), _ptr(scale), M, K, _ptr(y), _elem_type(y, "y"))
+    return y
+
+
+def pack_weights_fp8(w, turned=False, qw=None, sw=None, qt=None, st=None):
+    """Weights (K x N, or E x K x N, float32, float16 or bfloat16) as 8-bit floating-point codes
+    with a power of two for each block of 128 x 128. Returns a dict with qw ((E x) N x K'
+    float8_e4m3fn) and sw ((E x) K'/128 x N'/128 float8_e8m0fnu) for the product x.w and, where
+    turned is true, qt ((E x) K x N') and st ((E x) N'/128 x K'/128), the same values for the
+    product of a gradient dy with the turned weights. Asynchronous."""
+    torch = _torch()
+    if not isinstance(w, torch.Tensor) or w.dim() not in (2, 3):
+        raise ValueError("w must be K x N or E x K x N")
+    _check(w, "w", w.dtype)
+    wt, dev = _elem_type(w, "w"), w.device
+    *lead, K, N = w.shape
+    Kp, Np = _padded(K), _padded(N)
+    qw = _out(qw, "qw", torch.float8_e4m3fn, (*lead, N, Kp), dev)
+    sw = _out(sw, "sw", torch.float8_e8m0fnu, (*lead, Kp // GROUP, Np // GROUP), dev)
+    if turned:
+        qt = _out(qt, "qt", torch.float8_e4m3fn, (*lead, K, Np), dev)
+        st = _out(st, "st", torch.float8_e8m0fnu, (*lead, Np // GROUP, Kp // GROUP), dev)
+    elif qt is not None or st is not None:
+        raise ValueError("qt and st are outputs of turned=True")
+    _on(dev, qw=qw, sw=sw, qt=qt, st=st)
+    _call("bgt_pack_weights_fp8", dev, _ptr(w), wt, lead[0] if lead else 1, K, N, _ptr(qw),
+          _ptr(sw), _ptr(qt), _ptr(st))
+    out = {"qw": qw, "sw": sw}
+    if turned:
+        out.update(qt=qt, st=st)
+    return out
+
+
+def w8a8_gemm_fp8(qx, sx, qw, sw, y=None, out_dtype=None):
+    """Y = X.W of rows (quantize_fp8) and weights (pack_weights_fp8) in 8-bit floating point;
+    y (M x N) in y's dtype, else out_dtype, else float32 (float16 and bfloat16 run at the full
+    8-bit rate). With dy's codes and the turned weights (qt, st): the gradient of x."""
+    torch = _torch()
+    M, Kp = _check_rows8(qx, sx, "qx")
+    N = _check_weights8(qw, sw, Kp)
+    y = _out(y, "y", (out_dtype or torch.float32) if y is None else y.dtype, (M, N), qx.device)
+    _on(qx.device, qw=qw, sw=sw, y=y)
+    _call("bgt_w8a8_gemm_fp8", qx.device, _ptr(qx), _ptr(sx), _ptr(qw), _ptr(sw), M, N, Kp, _ptr(y),
+          _elem_type(y, "y"))
+    return y
+
+
+def w8a8_linear_fp8(x, qw, sw, qx=None, sx=None, y=None, out_dtype=None):
+    """quantize_fp8 of x (M x K), then w8a8_gemm_fp8, y in y's dtype, else out_dtype, else x's.
+    One launch for few rows. Returns (y, qx, sx): the codes are what wgrad_fp8 takes."""
+    torch = _torch()
+    M, K, ld = _rows(x, "x")
+    xt, dev, Kp = _elem_type(x, "x"), x.device, _padded(K)
+    N = _check_weights8(qw, sw, Kp)
+    qx = _out(qx, "qx", torch.float8_e4m3fn, (M, Kp), dev)
+    sx = _out(sx, "sx", torch.float8_e8m0fnu, (Kp // GROUP, M), dev)
+    y = _out(y, "y", (out_dtype or x.dtype) if y is None else y.dtype, (M, N), dev)
+    _on(dev, qw=qw, sw=sw, qx=qx, sx=sx, y=y)
+    _call("bgt_w8a8_linear_fp8", dev, _ptr(x), xt, ld, _ptr(qw), _ptr(sw), M, N, K, _ptr(qx),
+          _ptr(sx), _ptr(y), _elem_type(y, "y"))
+    return y, qx, sx
+
+
+def _check_slots(offsets, slot_token, dev):
+    torch = _torch()
+    _check(offsets, "offsets", torch.int32)
+    _check(slot_token, "slot_token", torch.int32)
+    _on(dev, offsets=offsets, slot_token=slot_token)
+    return offsets.numel() - 1, slot_token.numel()
+
+
+def w8a8_moe_gemm_fp8(qx, sx, offsets, slot_token, qw, sw, y=None, out_dtype=None):
+    """w8a8_gemm_fp8 for routed slots: row r of y (R x N) is row slot_token[r] of (qx, sx) times
+    the weights (E x N x K') of the expert whose offsets hold r; rows past offsets[-1] are
+    zero."""
+    torch = _torch()
+    T, Kp = _check_rows8(qx, sx, "qx")
+    E, R = _check_slots(offsets, slot_token, qx.device)
+    N = _check_weights8(qw, sw, Kp, E)
+    y = _out(y, "y", (out_dtype or torch.float32) if y is None else y.dtype, (R, N), qx.device)
+    _on(qx.device, qw=qw, sw=sw, y=y)
+    _call("bgt_w8a8_moe_gemm_fp8", qx.device, _ptr(qx), _ptr(sx), T, _ptr(offsets), _ptr(slot_token),
+          E, R, _ptr(qw), _ptr(sw), N, Kp, _ptr(y), _elem_type(y, "y"))
+    return y
+
+
+def wgrad_fp8(qx, sx, dy, K=None, dw=None):
+    """Gradient of a weight matrix, x^T dy (K x N, dy's dtype), from the rows of x kept in 8 bits
+    (quantize_fp8; K None: the padded size) and dy (M x N float32, float16 or bfloat16)."""
+    torch = _torch()
+    M, Kp = _check_rows8(qx, sx, "qx")
+    K, dev = _logical(K, Kp), qx.device
+    rows, N, ld = _rows(dy, "dy")
+    if rows != M:
+        raise ValueError(f"dy must have {M} rows, got {rows}")
+    dt = _elem_type(dy, "dy")
+    dw = _out(dw, "dw", dy.dtype, (K, N), dev)
+    need = lib().bgt_wgrad_fp8_workspace_bytes(M, K, N)
+    _raise("bgt_wgrad_fp8_workspace_bytes", need if need < 0 else 0)
+    ws = torch.empty(need // 4, dtype=torch.float32, device=dev) if need else None
+    _on(dev, dy=dy, dw=dw)
+    _call("bgt_wgrad_fp8", dev, _ptr(qx), _ptr(sx), _ptr(dy), dt, ld, M, K, N, _ptr(dw), _ptr(ws), need)
+    return dw
+
+
+def moe_wgrad_fp8(qx, sx, offsets, slot_token, dy, K=None, dw=None):
+    """Gradients of every expert's weights (E x K x N, dy's dtype): expert e's is the sum over
+    its slots r of row slot_token[r] of (qx, sx), turned, times row r of dy (R x N). Zero for an
+    expert without slots; rows of dy past offsets[-1] are not read."""
+    T, Kp = _check_rows8(qx, sx, "qx")
+    K, dev = _logical(K, Kp), qx.device
+    E, R = _check_slots(offsets, slot_token, dev)
+    rows, N, ld = _rows(dy, "dy")
+    if rows != R:
+        raise ValueError(f"dy must have {R} rows, got {rows}")
+    dt = _elem_type(dy, "dy")
+    dw = _out(dw, "dw", dy.dtype, (E, K, N), dev)
+    _on(dev, dy=dy, dw=dw)
+    _call("bgt_moe_wgrad_fp8", dev, _ptr(qx), _ptr(sx), T, _ptr(offsets), _ptr(slot_token), E, R,
+          _ptr(dy), dt, ld, K, N, _ptr(dw))
+    return dw
+
+
+def silu_mul_fp8(gate, up, hq=None, hs=None, gq=None, gs=None, uq=None, us=None):
+    """h = silu(gate) * up (M x K, one dtype; row strides may differ) as codes and scales of
+    quantize_fp8's form, and gate and up in that form too, which is what
+    silu_mul_fp8_backward takes. Returns (hq, hs, gq, gs, uq, us)."""
+    torch = _torch()
+    M, K, ldg = _rows(gate, "gate")
+    rows, cols, ldu = _rows(up, "up")
+    if (rows, cols) != (M, K) or up.dtype != gate.dtype:
+        raise ValueError("gate and up must have one shape and dtype")
+    t, dev, Kp = _elem_type(gate, "gate"), gate.device, _padded(K)
+    q = [_out(v, n, torch.float8_e4m3fn, (M, Kp), dev) for v, n in ((hq, "hq"), (gq, "gq"), (uq, "uq"))]
+    s = [_out(v, n, torch.float8_e8m0fnu, (Kp // GROUP, M), dev) for v, n in ((hs, "hs"), (gs, "gs"), (us, "us"))]
+    _on(dev, up=up, hq=q[0], gq=q[1], uq=q[2], hs=s[0], gs=s[1], us=s[2])
+    out = (q[0], s[0], q[1], s[1], q[2], s[2])
+    _call("bgt_silu_mul_fp8", dev, _ptr(gate), ldg, _ptr(up), ldu, t, M, K, *map(_ptr, out))
+    return out
+
+
+def silu_mul_fp8_backward(dh, gq, gs, uq, us, dgate=None, dup=None):
+    """Gradients (dgate, dup) of silu_mul_fp8's inputs (M x K, dh's dtype) from that of h and the
+    kept gate and up."""
+    M, K, ld = _rows(dh, "dh")
+    t, dev, Kp = _elem_type(dh, "dh"), dh.device, _padded(K)
+    _check_rows8(gq, gs, "gq", M, Kp)
+    _check_rows8(uq, us, "uq", M, Kp)
+    dgate = _out(dgate, "dgate", dh.dtype, (M, K), dev)
+    dup = _out(dup, "dup", dh.dtype, (M, K), dev)
+    _on(dev, gq=gq, uq=uq, dgate=dgate, dup=dup)
+    _call("bgt_silu_mul_fp8_backward", dev, _ptr(dh), t, ld, _ptr(gq), _ptr(gs), _ptr(uq), _ptr(us),
+          M, K, _ptr(dgate), _ptr(dup))
+    return dgate, dup
+
+
+# --------------------------------------------------------- balance loss of a router
+def moe_balance(logits, ids, loss=None, counts=None, probs=None, tokens=None):
+    """Balance loss E * sum_e f_e P_e of a router: f the share of the places in ids (T x k int32,
+    as moe_route leaves them) that are expert e's, P_e the mean over the tokens of the softmax
+    of logits (T x E) over all experts; tokens whose logits are all -inf count nowhere.
+    Returns (loss, counts, probs, tokens): a float32 scalar, the places of each expert (E
+    int32), P (E float32) and the number of tokens counted (1 int32), all on the device."""
+    torch = _torch()
+    T, E, ld = _rows(logits, "logits")
+    lt, dev = _elem_type(logits, "logits"), logits.device
+    _check(ids, "ids", torch.int32)
+    if ids.dim() != 2 or ids.shape[0] != T:
+        raise ValueError("ids must be T x k")
+    k = ids.shape[1]
+    need = lib().bgt_moe_balance_workspace_bytes(T, E)
+    _raise("bgt_moe_balance_workspace_bytes", need if need < 0 else 0)
+    ws = torch.empty(need // 4, dtype=torch.int32, device=dev)
+    loss = torch.empty((), dtype=torch.float32, device=dev) if loss is None else loss
+    _check(loss, "loss", torch.float32, ())
+    counts = _out(counts, "counts", torch.int32, (E,), dev)
+    probs = _out(probs, "probs", torch.float32, (E,), dev)
+    tokens = _out(tokens, "tokens", torch.int32, (1,), dev)
+    _on(dev, ids=ids, loss=loss, counts=counts, probs=probs, tokens=tokens)
+    _call("bgt_moe_balance", dev, _ptr(logits), lt, ld, _ptr(ids), T, E, k, _ptr(loss), _ptr(counts),
+          _ptr(probs), _ptr(tokens), _ptr(ws), need)
+    return loss, counts, probs, tokens
+
+
+def moe_balance_backward(dloss, logits, counts, tokens, dlogits=None):
+    """Gradient of the logits (their dtype, T x E) from that of moe_balance's loss (a float32
+    scalar on the device) with its counts and tokens (or their sums over a job's ranks)."""
+    torch = _torch()
+    T, E, ld = _rows(logits, "logits")
+    lt, dev = _elem_type(logits, "logits"), logits.device
+    _check(dloss, "dloss", torch.float32)
+    if dloss.numel() != 1:
+        raise ValueError("dloss must be one value")
+    _check(counts, "counts", torch.int32, (E,))
+    _check(tokens, "tokens", torch.int32, (1,))
+    dlogits = _out(dlogits, "dlogits", logits.dtype, (T, E), dev)
+    _on(dev, dloss=dloss, counts=counts, tokens=tokens, dlogits=dlogits)
+    _call("bgt_moe_balance_backward", dev, _ptr(dloss), _ptr(logits), lt, ld, _ptr(counts),
+          _ptr(tokens), T, E, _ptr(dlogits))
+    return dlogits

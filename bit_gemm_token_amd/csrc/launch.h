@@ -143,4 +143,47 @@ hipError_t launch_w4a16_moe(const void* x, int x_type, int64_t ldx, int64_t T, c
                             const int32_t* tok, int64_t E, int64_t R, const uint8_t* packed,
                             const float* fscale, int64_t N, int64_t K, OutY y, hipStream_t stream);
 
+// whether a launch of `wgs` workgroups of `threads` stays within the grid's 2^32 - 1 threads a
+// dimension; launchers of the operators below return hipErrorInvalidConfiguration otherwise
+inline bool grid_fits(int64_t wgs, int64_t threads) { return wgs * threads < (int64_t{1} << 32); }
+
+// ---- e4m3 codes with a power of two per block (quant_fp8.hip, gemm_fp8.hip, wgrad_fp8.hip);
+// K or N is the logical size, codes are padded to whole blocks of 128
+hipError_t launch_f8_rows(const void* x, int type, int64_t M, int64_t K, int64_t ld, uint8_t* q,
+                          uint8_t* scale, hipStream_t stream);
+hipError_t launch_f8_values(const uint8_t* q, const uint8_t* scale, int64_t M, int64_t K, void* y,
+                            int type, hipStream_t stream);
+hipError_t launch_f8_weights(const void* w, int type, int64_t E, int64_t K, int64_t N, uint8_t* qw,
+                             uint8_t* sw, uint8_t* qt, uint8_t* st, hipStream_t stream);
+hipError_t launch_f8_gate(const void* gate, int64_t ldg, const void* up, int64_t ldu, int type,
+                          int64_t M, int64_t K, uint8_t* hq, uint8_t* hs, uint8_t* gq, uint8_t* gs,
+                          uint8_t* uq, uint8_t* us, hipStream_t stream);
+hipError_t launch_f8_gate_grad(const void* dh, int64_t ld, int type, const uint8_t* gq,
+                               const uint8_t* gs, const uint8_t* uq, const uint8_t* us, int64_t M,
+                               int64_t K, void* dg, void* du, hipStream_t stream);
+// products: K a multiple of 128 (the padded size); Kx the elements of an unquantized row
+hipError_t launch_w8a8_f8(const uint8_t* qx, const uint8_t* sx, const uint8_t* qw,
+                          const uint8_t* sw, int64_t M, int64_t N, int64_t K, OutY y,
+                          hipStream_t stream);
+hipError_t launch_w8a8_f8_moe(const uint8_t* qx, const uint8_t* sx, const uint8_t* qw,
+                              const uint8_t* sw, int64_t N, int64_t K, const Route& rt, OutY y,
+                              hipStream_t stream);
+hipError_t launch_w8a8_f8_linear(const void* x, int type, int64_t ldx, int64_t Kx, const uint8_t* qw,
+                                 const uint8_t* sw, int64_t M, int64_t N, int64_t K, uint8_t* q,
+                                 uint8_t* s, OutY y, hipStream_t stream);
+// dw = values(qx)^T dy for one matrix (rt.E == 0) or each expert of a route; ws: fp32 parts
+int64_t f8_wgrad_ws_bytes(int64_t M, int64_t K, int64_t N, int64_t E);
+hipError_t launch_f8_wgrad(const uint8_t* qx, const uint8_t* sx, const void* dy, int64_t ld,
+                           int64_t M, int64_t K, int64_t N, const Route& rt, OutY dw, void* ws,
+                           hipStream_t stream);
+
+// ---- balance loss of a router (moe_balance.hip)
+int64_t moe_balance_ws_bytes(int64_t T, int64_t E);
+hipError_t launch_moe_balance(const void* logits, int type, int64_t ld, const int32_t* ids,
+                              int64_t T, int64_t E, int64_t k, float* loss, int32_t* counts,
+                              float* probs, int32_t* tokens, void* ws, hipStream_t stream);
+hipError_t launch_moe_balance_backward(const float* dloss, const void* logits, int type, int64_t ld,
+                                       const int32_t* counts, const int32_t* tokens, int64_t T,
+                                       int64_t E, void* dlogits, hipStream_t stream);
+
 }  // namespace bgt

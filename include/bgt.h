@@ -4,7 +4,8 @@
  * zero-point W8A8), two variants of the same epilogue: fine-grained W8A8
  * with integer scales and the grouped (mixture-of-experts) W4A8 GEMM, and the
  * mixture-of-experts layer around it: routing, rows to expert order and back,
- * and weight-only products of few rows.
+ * weight-only products of few rows, and 8-bit floating-point rows, weights and
+ * products for training and serving, with a router's balance loss.
  *
  * Pages cited:
  *   [IS] "Integer Scale: A Free Lunch for Faster Fine-grained Quantization of
@@ -530,6 +531,133 @@ int bgt_w4a16_moe_gemv(const void* x, int x_type, int64_t ldx, int64_t T,
                        int64_t R, const uint8_t* packed, const float* fscale, int64_t N, int64_t K,
                        void* y, int y_type, void* stream);
 
+/*
+ * Rows and weights in 8-bit floating point, with a scale for each block of 128, their products,
+ * and what a training step keeps of its activations and does with it in the backward pass.
+ * The pages' fine-grained scheme ([IS] 動機 3.1, [QB] §2.3.3: one scale for 128 elements) with
+ * floating codes: values are q * 2^e, q an e4m3 code (finite up to 448, no infinities), 2^e a
+ * power of two for each block, held as one exponent byte e + 127 (e8m0; 255 is NaN).
+ *     rows     M x K: codes M x K', exponents (K'/128) x M (block by block, the rows' bytes
+ *              contiguous); K' is K rounded up to a multiple of 128, codes behind K are zero
+ *     weights  K x N: qw, N x K' (column n's codes contiguous), sw, (K'/128) x (N'/128), one
+ *              exponent for 128 x 128 elements: for the product over K; and, if wanted, turned:
+ *              qt, K x N', st, (N'/128) x (K'/128), the same codes for the product over N
+ *              (the gradient of x). Of E experts one after the other.
+ * e is the least with max |x| <= 448 * 2^e, at least -117; codes are x / 2^e to nearest even,
+ * so that a value is off by at most 2^-4 of itself or 2^-10 * 2^e, and a block of zeros is
+ * exact. A block that holds an infinity or a NaN has the NaN exponent: all of its values are
+ * NaN. Other codes and exponents than these calls write are accepted too; where products leave
+ * fp32's normal range they may be flushed to zero.
+ * Common requirements: 1 <= M, T, R <= 2^24 rows, 1 <= K, N <= 2^18, 1 <= E <= 256; code
+ * matrices 16-byte aligned, other pointers aligned to their elements (16-byte aligned rows that
+ * are whole multiples of 16 bytes are faster). Sizes whose launch would pass 2^32 threads are
+ * refused with BGT_ERR_SHAPE. Every result is a fixed order of operations.
+ *
+ * bgt_quantize_fp8 -- rows into codes. x: M x K of x_type, row stride ldx >= K.
+ */
+int bgt_quantize_fp8(const void* x, int x_type, int64_t M, int64_t K, int64_t ldx, uint8_t* q,
+                     uint8_t* scale, void* stream);
+
+/* bgt_dequantize_fp8 -- the values that codes stand for, y: M x K of y_type, rounded once. */
+int bgt_dequantize_fp8(const uint8_t* q, const uint8_t* scale, int64_t M, int64_t K, void* y,
+                       int y_type, void* stream);
+
+/* bgt_pack_weights_fp8 -- weights into codes: w: E x K x N of w_type, dense. qt and st: both
+ * or neither (NULL). Asynchronous. */
+int bgt_pack_weights_fp8(const void* w, int w_type, int64_t E, int64_t K, int64_t N, uint8_t* qw,
+                         uint8_t* sw, uint8_t* qt, uint8_t* st, void* stream);
+
+/*
+ * bgt_w8a8_gemm_fp8 -- y = X.W of such rows and weights, y: M x N of y_type:
+ *     y_mn = sum over blocks g of 2^(a_gm + b_gn) sum_{k in g} qx_mk qw_nk
+ * in fp32, rounded once. fp16 and bf16 outputs are computed by the 8-bit matrix instructions,
+ * whose sums over a few k keep 13 bits below the largest product (an error of about 2^-16 of
+ * the sum of magnitudes, far below the rounding); fp32 outputs from exact products, at less
+ * than half the rate. For the gradient of x pass dy's codes and the turned weights (K and N
+ * exchanged).
+ */
+int bgt_w8a8_gemm_fp8(const uint8_t* qx, const uint8_t* sx, const uint8_t* qw, const uint8_t* sw,
+                      int64_t M, int64_t N, int64_t K, void* y, int y_type, void* stream);
+
+/* bgt_w8a8_linear_fp8 -- bgt_quantize_fp8 of x into qx, sx, then bgt_w8a8_gemm_fp8; one launch
+ * for few rows. */
+int bgt_w8a8_linear_fp8(const void* x, int x_type, int64_t ldx, const uint8_t* qw,
+                        const uint8_t* sw, int64_t M, int64_t N, int64_t K, uint8_t* qx,
+                        uint8_t* sx, void* y, int y_type, void* stream);
+
+/* bgt_w8a8_moe_gemm_fp8 -- the same for routed slots: y[r] = row slot_token[r] of (qx, sx)
+ * (T rows) times expert e's weights, for offsets and slots as in bgt_moe_route; rows
+ * expert_offsets[E] .. R-1 of y are zero. R <= T*E. Offsets are clamped to [0, R], tokens to
+ * [0, T-1], so other lists cannot reach outside the buffers, but leave rows unspecified. */
+int bgt_w8a8_moe_gemm_fp8(const uint8_t* qx, const uint8_t* sx, int64_t T,
+                          const int32_t* expert_offsets, const int32_t* slot_token, int64_t E,
+                          int64_t R, const uint8_t* qw, const uint8_t* sw, int64_t N, int64_t K,
+                          void* y, int y_type, void* stream);
+
+/*
+ * bgt_wgrad_fp8 -- gradient of a weight matrix from the rows kept in 8 bits:
+ *     dw_kn = sum_m (2^a_{k/128,m} qx_mk) dy_mn,      dw: K x N,
+ * qx, sx: M rows of K as bgt_quantize_fp8 wrote them for the product, dy: M x N, row stride
+ * lddy >= N; dy and dw of `type`. Products are exact (dy enters as one, two or three bf16
+ * terms), sums fp32. ws: bgt_wgrad_fp8_workspace_bytes(M, K, N) bytes of scratch, caller-owned
+ * (may be NULL where that is 0), used within the call only.
+ */
+int bgt_wgrad_fp8(const uint8_t* qx, const uint8_t* sx, const void* dy, int type, int64_t lddy,
+                  int64_t M, int64_t K, int64_t N, void* dw, void* ws, int64_t ws_bytes,
+                  void* stream);
+int64_t bgt_wgrad_fp8_workspace_bytes(int64_t M, int64_t K, int64_t N);
+
+/* bgt_moe_wgrad_fp8 -- the same for every expert over its slots: dw (E x K x N) of expert e is
+ * the sum over r = offs[e] .. offs[e+1]-1 of row slot_token[r] of (qx, sx) (T rows) times row r
+ * of dy (R rows); zero for an expert without slots. Rows of dy past offs[E] are not read. */
+int bgt_moe_wgrad_fp8(const uint8_t* qx, const uint8_t* sx, int64_t T,
+                      const int32_t* expert_offsets, const int32_t* slot_token, int64_t E,
+                      int64_t R, const void* dy, int type, int64_t lddy, int64_t K, int64_t N,
+                      void* dw, void* stream);
+
+/*
+ * bgt_silu_mul_fp8 -- the gated activation of a feed-forward layer, h = silu(g) * u with
+ * silu(g) = g / (1 + exp(-g)), computed in fp32 and stored as rows in 8 bits (the next
+ * product's operand), together with g and u in 8 bits, which is all that the backward call
+ * needs. gate, up: M x K of `type`, row strides ldg, ldu >= K (two halves of one matrix, say).
+ */
+int bgt_silu_mul_fp8(const void* gate, int64_t ldg, const void* up, int64_t ldu, int type,
+                     int64_t M, int64_t K, uint8_t* hq, uint8_t* hs, uint8_t* gq, uint8_t* gs,
+                     uint8_t* uq, uint8_t* us, void* stream);
+
+/* bgt_silu_mul_fp8_backward -- with g and u the kept values, s = 1 / (1 + exp(-g)):
+ *     dg = dh u s (1 + g (1 - s)),   du = dh g s,
+ * in fp32, rounded once; dh: row stride ld >= K, dg, du: dense, all M x K of `type`. */
+int bgt_silu_mul_fp8_backward(const void* dh, int type, int64_t ld, const uint8_t* gq,
+                              const uint8_t* gs, const uint8_t* uq, const uint8_t* us, int64_t M,
+                              int64_t K, void* dg, void* du, void* stream);
+
+/*
+ * bgt_moe_balance -- balance loss of a router, with the experts' counts: with p_t the softmax
+ * of token t's logits over all E experts, c_e the number of ids equal to e, f_e = c_e / sum c,
+ *     P_e = (1/T') sum_t p_te,   loss = E sum_e f_e P_e   (1 where both are even),
+ * T' the tokens that have a logit above -inf; the others (padding) have p_t = 0. ids outside
+ * [0, E) are no expert's. 0 where no token or no id is left. fp32 sums of at most a workgroup's
+ * tokens, added up in fp64. NaN logits and logits of +inf make p_t NaN as the formula does.
+ *   logits  T x E of `type`, row stride ld >= E;  ids  T x k int32 (as bgt_moe_route leaves them)
+ *   loss    one float32;  counts  E int32;  probs  E float32, P_e;  tokens  one int32, T'
+ *   ws      bgt_moe_balance_workspace_bytes(T, E) bytes of scratch, caller-owned.
+ * Requirements: 1 <= E <= 256, 1 <= k <= min(E, 16), T*k <= 2^24.
+ */
+int bgt_moe_balance(const void* logits, int type, int64_t ld, const int32_t* ids, int64_t T,
+                    int64_t E, int64_t k, float* loss, int32_t* counts, float* probs,
+                    int32_t* tokens, void* ws, int64_t ws_bytes, void* stream);
+int64_t bgt_moe_balance_workspace_bytes(int64_t T, int64_t E);
+
+/* bgt_moe_balance_backward -- gradient of the logits from that of the loss (one float32 on the
+ * device), counts being constants:
+ *     dl_te = dloss (E/T') p_te (f_e - sum_j f_j p_tj),   zeros for tokens without a logit
+ * above -inf. counts and tokens: the forward call's, or their sums over the ranks of a job.
+ * dlogits: T x E of `type`, dense. */
+int bgt_moe_balance_backward(const float* dloss, const void* logits, int type, int64_t ld,
+                             const int32_t* counts, const int32_t* tokens, int64_t T, int64_t E,
+                             void* dlogits, void* stream);
+
 /* Human-readable text of a status code (static storage). */
 const char* bgt_status_string(int status);
 
@@ -539,8 +667,8 @@ const char* bgt_status_string(int status);
  * 105 the grouped (mixture-of-experts) W4A8 integer-scale GEMM, 106 the
  * expert count and slot count in bgt_w4a8_moe_kernel_name, 107 the canonical
  * int4 layout (bgt_repack_int4_canonical), 108 bgt_set_prefill_kernel and
- * bgt_w4a8_workspace_bytes, 109 bgt_w4a8_gemm_is_noalloc. The bgt_moe_* and
- * bgt_w4a16_* entry points came after 109 as symbols of their own, with no
+ * bgt_w4a8_workspace_bytes, 109 bgt_w4a8_gemm_is_noalloc. The bgt_moe_*,
+ * bgt_w4a16_* and 8-bit floating-point (*_fp8) entry points came after 109 as symbols of their own, with no
  * change to what 109 names, and are found by their symbols. */
 int bgt_abi_version(void);
 
