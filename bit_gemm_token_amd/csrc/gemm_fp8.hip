@@ -53,205 +53,331 @@ __device__ __forceinline__ void zero_rows(const Route& rt, int N, OutY y, int z,
 }
 constexpr int kZeroWgs = 64;
 
-// waves of a streaming workgroup with so many 16 x 16 blocks: registers
-constexpr int stream_most(int blocks) { return blocks > 4 ? 8 : 16; }
+// waves of a streaming workgroup at most: sixteen of 128 registers, or eight of 256 for 64 rows,
+// whose fragments take 32 registers a group, and for chunks, whose next part of x takes as many
+// again
+constexpr int stream_waves(int mt, bool ch) { return mt == 4 || ch ? 8 : 16; }
+
+// blocks of bm rows of all experts' slots
+__device__ __forceinline__ int route_blocks(const Route& rt, int bm) {
+  int n = 0;
+  for (int base = 0; base < rt.E; base += kWave)
+    n += wave_sum(expert_row_tiles(rt, base + (int)threadIdx.x % kWave, bm));
+  return __builtin_amdgcn_readfirstlane(n);
+}
+// block b of them: its expert e, that one's first slot a and slots, and the block tm within
+__device__ __forceinline__ void route_block(const Route& rt, int bm, int b, int& e, int& a, int& rows,
+                                            int& tm) {
+  const int lane = threadIdx.x % kWave;
+  for (int base = 0; base < rt.E; base += kWave) {
+    const int nt = expert_row_tiles(rt, base + lane, bm);
+    int incl = nt;
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+      const int v = __shfl_up(incl, o, kWave);
+      if (lane >= o) incl += v;
+    }
+    const unsigned long long hit = __ballot(b >= incl - nt && b < incl);
+    if (hit != 0ull) {
+      const int l = (int)__builtin_ctzll(hit);
+      e = __builtin_amdgcn_readfirstlane(base + l);
+      tm = __builtin_amdgcn_readfirstlane(b - __shfl(incl - nt, l, kWave));
+      a = clamp_route(rt.offs[e], 0, rt.R);
+      rows = clamp_route(rt.offs[e + 1], a, rt.R) - a;
+      return;
+    }
+    b -= __builtin_amdgcn_readfirstlane(__shfl(incl, kWave - 1, kWave));
+  }
+  e = a = rows = tm = 0;                              // no such block
+}
 
 }  // namespace
 
 // =====================================================================
 // Few rows: the weights stream once through registers
 // =====================================================================
-// A workgroup takes 16 NT weight rows (outputs n) and 16 MT rows of x; its waves take the groups
-// in turn, keep D of them in flight in registers, and their sums meet in LDS in wave order.
-// XT >= 0: x comes as elements of that type and every wave turns its own groups' blocks into
-// codes (a block's scale needs no other wave); the workgroups of the first weight rows write
-// codes and scales out.
-template <int NT, int MT, int D, bool EX, int XT, bool GR>
-__global__ __launch_bounds__(stream_most(NT * MT) * 64) void k_f8_stream(
+// An item is 16 weight rows (outputs n) for one block of 16 MT rows of x. A workgroup takes a run
+// of items, weight rows innermost; its KS waves share the groups of K, GPW of each at a time.
+//   CH false  KS * GPW groups are all of K: a wave keeps its groups' fragments of x in
+//             registers over the run, so x is read once a workgroup, not once an item
+//   CH true   longer K: chunks of KS * GPW groups, each with its part of x
+// The next step's weights (and part of x) are on their way in registers. The waves' sums meet in
+// LDS (two buffers, one barrier an item) in wave order; an output is stored one item late,
+// before new loads are issued, so that no wait for loads waits for a store too.
+//
+// Of x whole 128-byte pieces of rows are loaded (reading 64 bytes of 16 rows an instruction, as
+// the fragments lie, took 6.2 us more than an empty launch for 64 rows x 4096 in every workgroup,
+// this 1.8) and become fragments by way of the wave's own LDS, 16-byte pieces XOR-swizzled by
+// row.
+// XT >= 0 (at most 16 rows): x comes as elements of that type and every wave turns its own
+// groups' blocks into codes (a block's scale needs no other wave); the workgroup of the first
+// item writes codes and scales out.
+template <int MT, int GPW, bool CH, bool EX, int XT, bool GR>
+__global__ __launch_bounds__(stream_waves(MT, CH) * 64) void k_f8_stream(
     const void* __restrict__ x, int64_t ldx, int Kx, const uint8_t* __restrict__ sx,
     const uint8_t* __restrict__ qw, const uint8_t* __restrict__ sw, int M, int N, int K, OutY y,
     Route rt, uint8_t* __restrict__ q_out, uint8_t* __restrict__ s_out) {
-  __shared__ float red[stream_most(NT * MT) * MT * 4 * 64];
+  constexpr int MOST = stream_waves(MT, CH);
+  __shared__ float red[2][MOST * MT * 4 * 64];
+  __shared__ __align__(16) uint8_t turn[MOST * MT * 2048];
   const int G = K / kGroup, B = (N + kGroup - 1) / kGroup;
   const int KS = blockDim.x / kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int lane = threadIdx.x % kWave;
   const int c = lane % 16, s4 = lane / 16;
-  const int ntn = (N + 16 * NT - 1) / (16 * NT);
-  int tn, tm, r0 = 0, rows = M;
-  if constexpr (GR) {
-    int e;
-    const int main_wgs = (int)gridDim.x - kZeroWgs;
-    if ((int)blockIdx.x >= main_wgs) {
-      zero_rows(rt, N, y, blockIdx.x - main_wgs, kZeroWgs);
-      return;
-    }
-    if (!grouped_tile(blockIdx.x, 16 * MT, ntn, rt, e, r0, rows, tm, tn)) return;
-    qw += e * rt.wstride;
-    sw += e * rt.sstride;
-  } else {
-    // the row blocks of one column of tiles follow each other on one XCD
-    const int ntm = (M + 16 * MT - 1) / (16 * MT), j = blockIdx.x / 8;
-    tn = j / ntm * 8 + blockIdx.x % 8;
-    tm = j % ntm;
-    if (tn >= ntn) return;
+  const int ntn = (N + 15) / 16;
+  const int main_wgs = (int)gridDim.x - (GR ? kZeroWgs : 0);
+  if (GR && (int)blockIdx.x >= main_wgs) {
+    zero_rows(rt, N, y, blockIdx.x - main_wgs, kZeroWgs);
+    return;
   }
-  const int n0 = tn * 16 * NT, m0 = tm * 16 * MT;
-
-  const uint8_t* wsrc[NT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int n = n0 + 16 * i + c;
-    wsrc[i] = qw + (int64_t)(n < N ? n : N - 1) * K + 16 * s4;
+  // 32-bit divisions, and none where there is nothing to divide: they precede the first load
+  const uint32_t wg = blockIdx.x, wgs = (uint32_t)main_wgs;
+  const uint32_t blocks = GR ? route_blocks(rt, 16 * MT) : (M + 16 * MT - 1) / (16 * MT);
+  const uint32_t total = blocks * (uint32_t)ntn;
+  uint32_t item = wg, last = wg + 1;
+  if (total != wgs) {                                 // an equal run each, one more for the first
+    const uint32_t each = total / wgs, more = total - each * wgs;
+    item = wg * each + (wg < more ? wg : more);
+    last = item + each + (wg < more ? 1 : 0);
   }
-  const uint8_t* ssrc = sw + n0 / kGroup;
-  int64_t row[MT];
-  bool live[MT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int m = m0 + 16 * i + c;
-    live[i] = m < rows;
-    row[i] = live[i] ? m : 0;
-    if constexpr (GR) row[i] = clamp_route(rt.tok[r0 + row[i]], 0, rt.T - 1);
+  if (item >= last) return;
+  int rb = 0, tn = (int)item;
+  if (blocks > 1) {
+    rb = (int)(item / (uint32_t)ntn);
+    tn = (int)(item - (uint32_t)rb * ntn);
   }
+  const int chunks = CH ? (G + KS * GPW - 1) / (KS * GPW) : 1;
   const int64_t Ms = GR ? rt.T : M;
 
-  constexpr int XW = XT < 0 ? 2 : (XT == kF32 ? 8 : 4);      // 16-byte pieces of x a lane and group
-  uint4 wb[D][NT][2], xb[D][MT][XW];
-  uint8_t sb[D], ab[D][MT];
-  auto fetch = [&](int j, int g) {
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        wb[j][i][h] = *reinterpret_cast<const uint4*>(wsrc[i] + (int64_t)g * kGroup + 64 * h);
-    sb[j] = ssrc[(int64_t)g * B];
+  // a block of rows: its expert, first slot (r0), row within (m0), rows of the expert
+  struct Block {
+    int e, r0, rows, m0;
+  };
+  auto locate = [&](int b) {
+    Block k{0, 0, M, b * 16 * MT};
+    if constexpr (GR) {
+      int tm;
+      route_block(rt, 16 * MT, b, k.e, k.r0, k.rows, tm);
+      k.m0 = tm * 16 * MT;
+    }
+    return k;
+  };
+  Block at = locate(rb);
+
+  // what is requested next: an item and, of long K, a chunk
+  uint32_t fitem = item;
+  int frb = rb, ftn = tn, fch = 0;
+  Block fat = at;
+  // rows of x as loaded (16 i + 8 h + lane / 8; -1: none) and of the scales (16 i + c)
+  int xrow[MT][2], srow[MT];
+  auto find_rows = [&](const Block& k) {
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
 #pragma unroll
-      for (int h = 0; h < XW; ++h) xb[j][i][h] = make_uint4(0, 0, 0, 0);
-      ab[j][i] = 0;
-      if constexpr (XT < 0) {
-        if (live[i]) {
-          const uint8_t* p = static_cast<const uint8_t*>(x) + row[i] * K + (int64_t)g * kGroup + 16 * s4;
-          xb[j][i][0] = *reinterpret_cast<const uint4*>(p);
-          xb[j][i][1] = *reinterpret_cast<const uint4*>(p + 64);
-          ab[j][i] = sx[(int64_t)g * Ms + row[i]];
-        }
-      } else {
-        constexpr int EB = XT == kF32 ? 4 : 2;
+      for (int h = 0; h < 2; ++h) {
+        const int m = k.m0 + 16 * i + 8 * h + lane / 8;
+        xrow[i][h] = m >= k.rows ? -1 : GR ? clamp_route(rt.tok[k.r0 + m], 0, rt.T - 1) : m;
+      }
+      const int m = k.m0 + 16 * i + c < k.rows ? k.m0 + 16 * i + c : k.rows - 1;
+      srow[i] = GR ? clamp_route(rt.tok[k.r0 + m], 0, rt.T - 1) : m;
+    }
+  };
+  uint4 wb[GPW][2], raw[GPW][MT][2];
+  uint32_t sb[GPW], sxb[GPW][MT], sraw[GPW][MT];
+  v8i xc[GPW][MT];
+  auto load_raw = [&](int ch) {
+#pragma unroll
+    for (int j = 0; j < GPW; ++j) {
+      const int g = (ch * GPW + j) * KS + wave;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int k = g * kGroup + 64 * h + 16 * s4;       // 16 elements, all there or none
-          if (live[i] && k < Kx) {
-            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(x) + (row[i] * ldx + k) * EB);
-#pragma unroll
-            for (int u = 0; u < XW / 2; ++u) xb[j][i][h * (XW / 2) + u] = p[u];
-          }
+          raw[j][i][h] = make_uint4(0, 0, 0, 0);
+          if (xrow[i][h] >= 0 && g < G)
+            raw[j][i][h] = *reinterpret_cast<const uint4*>(
+                static_cast<const uint8_t*>(x) + (int64_t)xrow[i][h] * K + (int64_t)g * kGroup + lane % 8 * 16);
         }
+        sraw[j][i] = sx[(int64_t)(g < G ? g : G - 1) * Ms + srow[i]];
       }
     }
   };
-  v4f acc[NT][MT];
+  // loads of weights are unconditional, so that they go to the registers the last step used up
+  // without copies: past the run's end all lanes read the weights' first bytes
+  auto fetch = [&]() {
+    const bool more = fitem < last;
+    const int n = 16 * ftn + c;
+    const uint8_t* p = qw + (GR ? fat.e * rt.wstride : 0);
+    const uint8_t* ps = sw + (GR ? fat.e * rt.sstride : 0);
+    p += more ? (int64_t)(n < N ? n : N - 1) * K + 16 * s4 : 0;
+    ps += more ? ftn / 8 : 0;
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) acc[i][m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-
-  auto compute = [&](int j, int g) {
-    v8i xc[MT];
-    uint32_t sxb[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      if constexpr (XT < 0) {
-        xc[i] = join(xb[j][i][0], xb[j][i][1]);
-        sxb[i] = ab[j][i];
-      } else {
-        float v[32];
-#pragma unroll
-        for (int u = 0; u < XW; ++u) {
-          const uint4 w = xb[j][i][u];
-          if constexpr (XT == kF32) {
-            v[4 * u + 0] = __uint_as_float(w.x); v[4 * u + 1] = __uint_as_float(w.y);
-            v[4 * u + 2] = __uint_as_float(w.z); v[4 * u + 3] = __uint_as_float(w.w);
-          } else {
-            const float4 a = widen_x4<XT>(make_uint2(w.x, w.y)), b = widen_x4<XT>(make_uint2(w.z, w.w));
-            v[8 * u + 0] = a.x; v[8 * u + 1] = a.y; v[8 * u + 2] = a.z; v[8 * u + 3] = a.w;
-            v[8 * u + 4] = b.x; v[8 * u + 5] = b.y; v[8 * u + 6] = b.z; v[8 * u + 7] = b.w;
-          }
-        }
-        uint32_t top = 0;
-#pragma unroll
-        for (int u = 0; u < 32; ++u) top = umax(top, abs_bits(v[u]));
-        top = umax(top, (uint32_t)__shfl_xor((int)top, 16, kWave));
-        top = umax(top, (uint32_t)__shfl_xor((int)top, 32, kWave));
-        const uint32_t byte = f8_scale_byte(top);
-        const float inv = f8_inverse(byte);
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-          xc[i][u] = (int)f8_pack4(v[4 * u] * inv, v[4 * u + 1] * inv, v[4 * u + 2] * inv, v[4 * u + 3] * inv);
-        sxb[i] = byte;
-        if (tn == 0 && live[i]) {
-          uint8_t* p = q_out + row[i] * K + (int64_t)g * kGroup + 16 * s4;
-          *reinterpret_cast<uint4*>(p) = make_uint4(xc[i][0], xc[i][1], xc[i][2], xc[i][3]);
-          *reinterpret_cast<uint4*>(p + 64) = make_uint4(xc[i][4], xc[i][5], xc[i][6], xc[i][7]);
-          if (s4 == 0) s_out[(int64_t)g * M + row[i]] = (uint8_t)byte;
-        }
-      }
+    for (int j = 0; j < GPW; ++j) {
+      // past the wave's groups: the last group again, which meets zero codes of x
+      int g = (fch * GPW + j) * KS + wave;
+      g = !more ? 0 : g < G ? g : G - 1;
+      sb[j] = ps[(int64_t)g * B];
+      wb[j][0] = *reinterpret_cast<const uint4*>(p + (int64_t)g * kGroup);
+      wb[j][1] = *reinterpret_cast<const uint4*>(p + (int64_t)g * kGroup + 64);
     }
+    if constexpr (CH && XT < 0)
+      if (more) load_raw(fch);
+    if (CH && ++fch < chunks) return;
+    fch = 0;
+    if (++fitem < last && ++ftn == ntn) {
+      ftn = 0;
+      fat = locate(++frb);
+      if constexpr (CH) find_rows(fat);
+    }
+  };
+  uint8_t* mine = turn + wave * MT * 2048;
+  auto place = [](int row, int piece) { return row * 128 + 16 * (piece ^ ((row >> 1) & 7)); };
+  auto read_x = [&](const uint8_t* p) {
+    return join(*reinterpret_cast<const uint4*>(p + place(c, s4)),
+                *reinterpret_cast<const uint4*>(p + place(c, s4 + 4)));
+  };
+  auto turn_x = [&]() {                               // raw -> fragments
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const v8i w = join(wb[j][i][0], wb[j][i][1]);
+    for (int j = 0; j < GPW; ++j) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        if constexpr (EX) {
-          v4f p = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int i = 0; i < MT; ++i) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(w, u), widen8(xc[m], u), p, 0, 0, 0);
-          const float a = f8_scale(sxb[m]), b = f8_scale(sb[j]);
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<uint4*>(mine + i * 2048 + place(8 * h + lane / 8, lane % 8)) = raw[j][i][h];
+        sxb[j][i] = sraw[j][i];
+      }
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[i][m][r] = acc[i][m][r] + p[r] * a * b;
-        } else {
-          acc[i][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, xc[m], acc[i][m], 0, 0, 0,
-                                                                       (int)sb[j], 0, (int)sxb[m]);
+      for (int i = 0; i < MT; ++i) xc[j][i] = read_x(mine + i * 2048);
+    }
+  };
+  // elements: rows 4 r + lane / 16, eight a lane, a block in 16 lanes
+  auto quantize_x = [&](int ch, bool write) {
+    if constexpr (XT >= 0) {
+#pragma unroll
+      for (int j = 0; j < GPW; ++j) {
+        const int g = (ch * GPW + j) * KS + wave;
+        sxb[j][0] = 127;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 4 * r + s4, k = g * kGroup + 8 * c;
+          uint32_t byte = 127;
+          uint2 q = make_uint2(0, 0);
+          if (4 * r < M) {                            // uniform
+            float v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = 0.0f;
+            if (row < M && g < G && k < Kx) load8<XT>(x, row * ldx + k, v);
+            uint32_t top = 0;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) top = umax(top, abs_bits(v[u]));
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) top = umax(top, (uint32_t)__shfl_xor((int)top, o, kWave));
+            byte = f8_scale_byte(top);
+            const float inv = f8_inverse(byte);
+            q.x = f8_pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+            q.y = f8_pack4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+            if (write && row < M && g < G) {
+              *reinterpret_cast<uint2*>(q_out + (int64_t)row * K + k) = q;
+              if (c == 0) s_out[(int64_t)g * M + row] = (uint8_t)byte;
+            }
+          }
+          *reinterpret_cast<uint2*>(mine + place(row, c / 2) + c % 2 * 8) = q;
+          // lane (c, s4) wants the byte of row c = 4 r + s: it lies in lanes 16 s ..
+          const uint32_t of = (uint32_t)__shfl((int)byte, c % 4 * 16, kWave);
+          if (c / 4 == r) sxb[j][0] = of;
         }
+        xc[j][0] = read_x(mine);
       }
     }
   };
 
-#pragma unroll
-  for (int j = 0; j < D; ++j)
-    if (wave + j * KS < G) fetch(j, wave + j * KS);
-#pragma unroll 1
-  for (int g = wave; g < G; g += D * KS) {
-#pragma unroll
-    for (int j = 0; j < D; ++j) {
-      if (g + j * KS < G) {
-        compute(j, g + j * KS);
-        if (g + (j + D) * KS < G) fetch(j, g + (j + D) * KS);
-      }
-    }
+  find_rows(at);
+  if constexpr (!CH && XT < 0) load_raw(0);
+  fetch();
+  if constexpr (!CH) {
+    if constexpr (XT < 0) turn_x();
+    else quantize_x(0, item == 0);
   }
-
-  // lane: row m = 16 mt + lane % 16, outputs n = 16 nt + 4 (lane / 16) + r
+  const bool single = (int)blockDim.x >= MT * 256;    // an output of an item a thread at most
+  int buf = 0;
+  int64_t late = -1;                                  // place and value of the output to store
+  float value = 0.0f;
+  auto sum = [&](int t, int64_t& o, float& v) {       // output t of the item over the waves
+    const int n = t % 16, m = t / 16;
+    const int of = (m / 16 * 4 + n % 4) * 64 + n / 4 * 16 + m % 16;
+    if (at.m0 + m >= at.rows || 16 * tn + n >= N) return;
+    v = 0.0f;
+    if (KS == MOST) {                                 // all reads at once
 #pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    if (i > 0) __syncthreads();
+      for (int w = 0; w < MOST; ++w) v += red[buf][w * MT * 256 + of];
+    } else {
+      for (int w = 0; w < KS; ++w) v += red[buf][w * MT * 256 + of];
+    }
+    o = (int64_t)(at.r0 + at.m0 + m) * N + 16 * tn + n;
+  };
+#pragma unroll 1
+  while (item < last) {
+    v4f acc[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+    for (int ch = 0; ch < chunks; ++ch) {
+      if constexpr (CH) {
+        if constexpr (XT < 0) turn_x();
+        else quantize_x(ch, item == 0);
+      }
+#pragma unroll
+      for (int j = 0; j < GPW; ++j) {
+        const v8i w = join(wb[j][0], wb[j][1]);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          if constexpr (EX) {
+            v4f p = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(w, u), widen8(xc[j][m], u), p, 0, 0, 0);
+            const float a = f8_scale(sxb[j][m]), b = f8_scale(sb[j]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[m][r] = acc[m][r] + p[r] * a * b;
+          } else {
+            acc[m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, xc[j][m], acc[m], 0, 0, 0,
+                                                                      (int)sb[j], 0, (int)sxb[j][m]);
+          }
+        }
+      }
+      if (late >= 0) y.put(late, value);
+      late = -1;
+      fetch();
+    }
+    // lane: row m = 16 mt + lane % 16, outputs n = 4 (lane / 16) + r
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) red[(wave * MT * 4 + m * 4 + r) * 64 + lane] = acc[i][m][r];
+      for (int r = 0; r < 4; ++r) red[buf][(wave * MT * 4 + m * 4 + r) * 64 + lane] = acc[m][r];
     __syncthreads();
-    for (int t = threadIdx.x; t < MT * 256; t += blockDim.x) {
-      const int n = t % 16, m = t / 16;
-      const int at = (m / 16 * 4 + n % 4) * 64 + n / 4 * 16 + m % 16;
-      if (m0 + m >= rows || n0 + 16 * i + n >= N) continue;
-      float v = 0.0f;
-      for (int w = 0; w < KS; ++w) v += red[w * MT * 256 + at];
-      y.put((int64_t)(r0 + m0 + m) * N + n0 + 16 * i + n, v);
+    if (single) {
+      if ((int)threadIdx.x < MT * 256) sum(threadIdx.x, late, value);
+    } else {
+      for (int t = threadIdx.x; t < MT * 256; t += blockDim.x) {
+        int64_t o = -1;
+        float v = 0.0f;
+        sum(t, o, v);
+        if (o >= 0) y.put(o, v);
+      }
+    }
+    buf ^= 1;
+    if (++item < last && ++tn == ntn) {
+      tn = 0;
+      at = locate(++rb);
+      if constexpr (!CH && XT < 0) {
+        find_rows(at);
+        load_raw(0);
+        turn_x();
+      }
     }
   }
+  if (late >= 0) y.put(late, value);
 }
 
 // =====================================================================
@@ -478,36 +604,48 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(2)
 // ------------------------------------------------------------------ launchers
 namespace {
 
-// waves of a streaming workgroup: as many as leave each two groups, at most `most`
-int stream_waves(int64_t G, int most) {
-  int ks = 1;
-  while (ks < most && 2 * ks * 2 <= G) ks *= 2;
-  return ks;
-}
-
-template <int NT, int MT, int D, bool EX, int XT, bool GR>
+// waves: as many as the groups; workgroups: enough for 16 waves a CU (8 for 64 rows: registers),
+// no more than items (of a route: than its slots may need)
+template <int MT, int GPW, bool CH, bool EX, int XT, bool GR>
 hipError_t stream_t(const void* x, int64_t ldx, int64_t Kx, const uint8_t* sx, const uint8_t* qw,
-              const uint8_t* sw, int64_t M, int64_t N, int64_t K, OutY y, const Route& rt,
-              uint8_t* q_out, uint8_t* s_out, hipStream_t stream) {
-  const int64_t ntn = (N + 16 * NT - 1) / (16 * NT);
-  const int64_t wgs = GR ? (rt.R / (16 * MT) + std::min<int64_t>(rt.E, rt.R)) * ntn + kZeroWgs
-                         : (ntn + 7) / 8 * 8 * ((M + 16 * MT - 1) / (16 * MT));
-  const int ks = stream_waves(K / kGroup, stream_most(NT * MT));
-  if (!grid_fits(wgs, ks * kWave)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((k_f8_stream<NT, MT, D, EX, XT, GR>), dim3((unsigned)wgs), dim3(ks * kWave), 0,
+                    const uint8_t* sw, int64_t M, int64_t N, int64_t K, OutY y, const Route& rt,
+                    uint8_t* q_out, uint8_t* s_out, hipStream_t stream) {
+  const int64_t G = K / kGroup;
+  int waves = 1;
+  while (waves < stream_waves(MT, CH) && waves < G) waves *= 2;
+  const int64_t blocks = GR ? rt.R / (16 * MT) + std::min<int64_t>(rt.E, rt.R) : (M + 16 * MT - 1) / (16 * MT);
+  const int64_t items = blocks * ((N + 15) / 16);
+  const int64_t wgs = std::min<int64_t>(items, device_cus() * ((MT == 4 ? 8 : 16) / waves)) + (GR ? kZeroWgs : 0);
+  if (items > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((k_f8_stream<MT, GPW, CH, EX, XT, GR>), dim3((unsigned)wgs), dim3(waves * kWave), 0,
                      stream, x, ldx, (int)Kx, sx, qw, sw, (int)M, (int)N, (int)K, y, rt, q_out, s_out);
   return hipGetLastError();
 }
 
+constexpr int kFusedRows = 8;                         // rows quantized by the product itself
+constexpr int kStreamGroups = 32;                     // groups of K whose x the waves keep
+constexpr int kStreamRows = 64;                       // rows of a matrix that this kernel takes
+
 template <bool EX, bool GR>
 hipError_t stream_rows(const uint8_t* qx, const uint8_t* sx, const uint8_t* qw, const uint8_t* sw,
-                 int64_t M, int64_t N, int64_t K, OutY y, const Route& rt, int64_t per,
-                 hipStream_t stream) {
-  if (per <= 16)
-    return stream_t<1, 1, 4, EX, -1, GR>(qx, K, K, sx, qw, sw, M, N, K, y, rt, nullptr, nullptr, stream);
-  if (per <= 32)
-    return stream_t<1, 2, 2, EX, -1, GR>(qx, K, K, sx, qw, sw, M, N, K, y, rt, nullptr, nullptr, stream);
-  return stream_t<2, 4, 1, EX, -1, GR>(qx, K, K, sx, qw, sw, M, N, K, y, rt, nullptr, nullptr, stream);
+                       int64_t M, int64_t N, int64_t K, OutY y, const Route& rt, int64_t per,
+                       hipStream_t stream) {
+  const bool all = K <= kStreamGroups * kGroup;       // 16 waves of 2 groups, 8 of 4
+  // experts' slots scatter about their mean, and one past the block reads its weights again
+  if (GR) per += per / 2;
+#define BGT_STREAM(MT, GPW, CH) \
+  return stream_t<MT, GPW, CH, EX, -1, GR>(qx, K, K, sx, qw, sw, M, N, K, y, rt, nullptr, nullptr, stream)
+  if (per <= 16) {
+    if (all) BGT_STREAM(1, 2, false);
+    BGT_STREAM(1, 2, true);
+  }
+  if (per <= 32) {
+    if (all) BGT_STREAM(2, 2, false);
+    BGT_STREAM(2, 2, true);
+  }
+  if (all) BGT_STREAM(4, 4, false);
+  BGT_STREAM(4, 2, true);
+#undef BGT_STREAM
 }
 
 template <int BN, int BM, int WN, int WM, bool EX, bool GR>
@@ -523,11 +661,11 @@ hipError_t tile_t(const uint8_t* qx, const uint8_t* sx, const uint8_t* qw, const
 }
 
 template <bool GR>
-hipError_t launch_t(const uint8_t* qx, const uint8_t* sx, const uint8_t* qw, const uint8_t* sw, int64_t M,
-              int64_t N, int64_t K, OutY y, const Route& rt, hipStream_t stream) {
+hipError_t launch_t(const uint8_t* qx, const uint8_t* sx, const uint8_t* qw, const uint8_t* sw,
+                    int64_t M, int64_t N, int64_t K, OutY y, const Route& rt, hipStream_t stream) {
   const bool ex = y.type == kF32;
   const int64_t per = GR ? (rt.R + rt.E - 1) / rt.E : M;      // rows of a matrix
-  if (per <= 256)
+  if (per <= kStreamRows)
     return ex ? stream_rows<true, GR>(qx, sx, qw, sw, M, N, K, y, rt, per, stream)
               : stream_rows<false, GR>(qx, sx, qw, sw, M, N, K, y, rt, per, stream);
   return ex ? tile_t<128, 128, 2, 4, true, GR>(qx, sx, qw, sw, M, N, K, y, rt, stream)
@@ -551,17 +689,19 @@ hipError_t launch_w8a8_f8_moe(const uint8_t* qx, const uint8_t* sx, const uint8_
 hipError_t launch_w8a8_f8_linear(const void* x, int type, int64_t ldx, int64_t Kx, const uint8_t* qw,
                                  const uint8_t* sw, int64_t M, int64_t N, int64_t K, uint8_t* q,
                                  uint8_t* s, OutY y, hipStream_t stream) {
-  const bool fused = M <= 16 && Kx % 16 == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0 &&
-                     ldx * (type == kF32 ? 4 : 2) % 16 == 0;
+  // quantized by the product where its waves keep x (8 rows x 4096 into 4096: 8.4 us, one launch
+  // more for the codes about 10), not for longer K, where every item would do it again
+  const bool fused = M <= kFusedRows && K <= kStreamGroups * kGroup && Kx % 8 == 0 &&
+                     reinterpret_cast<uintptr_t>(x) % 16 == 0 && ldx * (type == kF32 ? 4 : 2) % 16 == 0;
   if (!fused) {
     const hipError_t e = launch_f8_rows(x, type, M, Kx, ldx, q, s, stream);
     return e != hipSuccess ? e : launch_w8a8_f8(q, s, qw, sw, M, N, K, y, stream);
   }
   const Route rt{};
   const bool ex = y.type == kF32;
-#define BGT_FUSED(T)                                                                               \
-  return ex ? stream_t<1, 1, 2, true, T, false>(x, ldx, Kx, nullptr, qw, sw, M, N, K, y, rt, q, s, stream) \
-            : stream_t<1, 1, 2, false, T, false>(x, ldx, Kx, nullptr, qw, sw, M, N, K, y, rt, q, s, stream)
+#define BGT_FUSED(T)                                                                                      \
+  return ex ? stream_t<1, 2, false, true, T, false>(x, ldx, Kx, nullptr, qw, sw, M, N, K, y, rt, q, s, stream) \
+            : stream_t<1, 2, false, false, T, false>(x, ldx, Kx, nullptr, qw, sw, M, N, K, y, rt, q, s, stream)
   if (type == kF32) BGT_FUSED(kF32);
   if (type == kF16) BGT_FUSED(kF16);
   BGT_FUSED(kBF16);
