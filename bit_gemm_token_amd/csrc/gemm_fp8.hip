@@ -561,6 +561,7 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(2)
   // 16 bits: the tile as BM rows of BN outputs in the stages' LDS, RPS rows a stage, 16-byte
   // pieces XOR-swizzled by row; then whole rows out
   constexpr int RPS = STG / (2 * BN);
+  constexpr int PIECES = BN / 8, SWZ = (PIECES < 16 ? PIECES : 16) - 1;
   static_assert(BM <= 2 * RPS, "the tile fits the stages");
   __syncthreads();                                    // every wave is done with the stages
 #pragma unroll
@@ -575,17 +576,16 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(2)
         const float *v = reinterpret_cast<const float*>(&acc[i][m]) + 4 * q;
         const uint2 w = y.type == kF16 ? make_uint2(narrow2<kF16>(v[0], v[1]), narrow2<kF16>(v[2], v[3]))
                                        : make_uint2(narrow2<kBF16>(v[0], v[1]), narrow2<kBF16>(v[2], v[3]));
-        *reinterpret_cast<uint2*>(p + 16 * (piece ^ (r & 15)) + 8 * hf) = w;
+        *reinterpret_cast<uint2*>(p + 16 * (piece ^ (r & SWZ)) + 8 * hf) = w;
       }
     }
   __syncthreads();
-  constexpr int PIECES = BN / 8;
   const bool vec = N % 8 == 0 && reinterpret_cast<uintptr_t>(y.p) % 16 == 0;
   uint16_t* yp = static_cast<uint16_t*>(y.p);
 #pragma unroll 4
   for (int t = tid; t < BM * PIECES; t += NW * 64) {
     const int r = t / PIECES, piece = t % PIECES;
-    const uint8_t* p = (r < RPS ? S0 : S1) + (r < RPS ? r : r - RPS) * (2 * BN) + 16 * (piece ^ (r & 15));
+    const uint8_t* p = (r < RPS ? S0 : S1) + (r < RPS ? r : r - RPS) * (2 * BN) + 16 * (piece ^ (r & SWZ));
     const uint4 v = *reinterpret_cast<const uint4*>(p);
     const int n = n0 + 8 * piece;
     if (m0 + r >= M || n >= N) continue;
@@ -668,8 +668,22 @@ hipError_t launch_t(const uint8_t* qx, const uint8_t* sx, const uint8_t* qw, con
   if (per <= kStreamRows)
     return ex ? stream_rows<true, GR>(qx, sx, qw, sw, M, N, K, y, rt, per, stream)
               : stream_rows<false, GR>(qx, sx, qw, sw, M, N, K, y, rt, per, stream);
-  return ex ? tile_t<128, 128, 2, 4, true, GR>(qx, sx, qw, sw, M, N, K, y, rt, stream)
-            : tile_t<256, 256, 2, 4, false, GR>(qx, sx, qw, sw, M, N, K, y, rt, stream);
+  if (ex) return tile_t<128, 128, 2, 4, true, GR>(qx, sx, qw, sw, M, N, K, y, rt, stream);
+  // The largest tile that keeps the CUs busy, one workgroup each of 256 x 256, two and more of the
+  // smaller ones (us): 8192 x 14336 into 4096, 512 tiles of 256 x 256: 393, of 128 x 128 459;
+  // 1024 x 4096 into 14336, 224 tiles: 62.6 and 71.6; 2048 x 4096 into 4096, 128 tiles: 55.3, 38.1;
+  // 512 x 4096 into 4096, 128 tiles of 128 x 128: 23.5, of 64 x 64 18.5. Experts' last tiles are
+  // half empty on average.
+  auto tiles = [&](int64_t t) {
+    const int64_t rows = GR ? (2 * rt.R / t + rt.E) / 2 : (M + t - 1) / t;
+    return rows * ((N + t - 1) / t);
+  };
+  const int64_t busy = (int64_t)device_cus() * 4 / 5;
+  if (tiles(256) >= busy && per >= 256)
+    return tile_t<256, 256, 4, 2, false, GR>(qx, sx, qw, sw, M, N, K, y, rt, stream);
+  if (tiles(128) >= busy)
+    return tile_t<128, 128, 2, 2, false, GR>(qx, sx, qw, sw, M, N, K, y, rt, stream);
+  return tile_t<64, 64, 2, 2, false, GR>(qx, sx, qw, sw, M, N, K, y, rt, stream);
 }
 
 }  // namespace
