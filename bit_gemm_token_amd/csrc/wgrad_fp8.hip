@@ -9,11 +9,12 @@
 // and the sum is fp32.
 //
 // Both operands lie with the summed index m outermost, while a matrix instruction wants eight
-// consecutive m of one column in a lane. A lane therefore loads two columns of eight rows
-// (whole rows are contiguous over the lanes, and a wave's rows and scales are uniform), pairs
-// rows with byte permutes, and writes 16-byte pieces [m / 8][column][8] to LDS, which are the
-// operands: reads and writes are 16 bytes a lane in lane order. Two LDS stages of 32 rows, the
-// next rows in registers, one barrier a step.
+// consecutive m of one column in a lane. They are kept in LDS as they lie, rows of columns, and
+// read through the transposing LDS read (four rows of 16 columns: a lane gets the four rows of
+// its column). 16-bit floats of the matrix product's own type go to LDS straight from memory
+// (aligned bf16 rows); codes and the other types pass through registers, a step ahead, where
+// they are widened or split. Rows are XOR-swizzled by 64 bytes so that the four rows of a read
+// lie on distinct banks. Two LDS stages, one barrier a step.
 #include <algorithm>
 
 #include "fp8_common.h"
@@ -26,37 +27,36 @@ namespace {
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef __bf16 v2b __attribute__((ext_vector_type(2)));
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
+typedef short v4s __attribute__((ext_vector_type(4)));
 
-constexpr int kStepRows = 32;
+enum { kByElement, kByPiece, kStraight };             // how dy's rows come
 
-// the high halves of two words, the first in the low half
-__device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) {
-  return __builtin_amdgcn_perm(b, a, 0x07060302u);
-}
-__device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) {
-  return __builtin_amdgcn_perm(b, a, 0x05040100u);
-}
-// leading 8 significant bits of v as a bf16 in the high half (a NaN stays one), and the rest
-__device__ __forceinline__ uint32_t lead(float v, float& rest) {
-  const uint32_t u = __float_as_uint(v);
-  const uint32_t h = (u & 0x7FFFFFFFu) > 0x7F800000u ? 0x7FC00000u : u & 0xFFFF0000u;
-  rest = (u & 0x7F800000u) == 0x7F800000u ? 0.0f : v - __uint_as_float(h);
-  return h;
+__device__ const uint4 kZeroPiece = {0, 0, 0, 0};     // what rows behind the last are read from
+
+// two leading parts of 8 significant bits as bf16, in one word each; v: what is left
+__device__ __forceinline__ uint32_t lead2(float& a, float& b) {
+  const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+  a -= __uint_as_float(ua & 0xFFFF0000u);
+  b -= __uint_as_float(ub & 0xFFFF0000u);
+  return __builtin_amdgcn_perm(ub, ua, 0x07060302u);
 }
 constexpr int terms_of(int type) { return type == kBF16 ? 1 : type == kF16 ? 2 : 3; }
 
 }  // namespace
 
-// S x S outputs of dW a workgroup (S / 32 waves); GR: blockIdx.y is the expert. parts > 1:
-// blockIdx.y is a part of the rows, whose fp32 sums go to part[y] (K x N).
-template <int S, int DT, bool VEC, bool GR>
+// S x S outputs of dW a workgroup (2 x S / 64 waves), ROWS rows a step; GR: blockIdx.y is the
+// expert. parts > 1: blockIdx.y is a part of the rows, whose fp32 sums go to part[y] (K x N).
+template <int S, int ROWS, int DT, int LOAD, bool GR>
 __global__ __launch_bounds__(S * 2) __attribute__((amdgpu_waves_per_eu(2))) void k_f8_wgrad(
     const uint8_t* __restrict__ qx, const uint8_t* __restrict__ sx, const void* __restrict__ dy,
     int64_t ld, int M, int K, int N, Route rt, OutY dw, int parts, float* __restrict__ part) {
-  constexpr int NW = S / 32, TERMS = terms_of(DT);
-  constexpr int WN = NW / 2;                          // 2 x WN waves
-  constexpr int FK = S / 2 / 32, FN = S / WN / 32;    // 32 x 32 blocks of a wave
-  constexpr int PANEL = 4 * S * 16;                   // 32 rows of S columns
+  static_assert(LOAD != kStraight || DT == kBF16, "only operands go straight to LDS");
+  constexpr int NT = S * 2, NW = NT / kWave, WN = S / 64, TERMS = terms_of(DT);
+  constexpr int FK = S / 2 / 32, FN = 2;              // 32 x 32 blocks of a wave
+  constexpr int ROW = S * 2, PANEL = ROWS * ROW;      // bytes
+  constexpr int PX = ROWS * S / 16 / NT;              // 16 codes of a row each, of a thread
+  constexpr int PY = ROWS * S / 8 / NT;               // 8 elements of a row of dy
+  constexpr int WY = DT == kF32 ? 8 : 4;              // words of these
   __shared__ __align__(16) uint8_t X0[PANEL];
   __shared__ __align__(16) uint8_t X1[PANEL];
   __shared__ __align__(16) uint8_t Y0[TERMS * PANEL];
@@ -75,100 +75,135 @@ __global__ __launch_bounds__(S * 2) __attribute__((amdgpu_waves_per_eu(2))) void
     to = clamp_route(rt.offs[blockIdx.y + 1], from, rt.R);
     out0 = (int64_t)blockIdx.y * K * N;
   } else if (parts > 1) {                             // whole steps to each part
-    const int steps = (M + kStepRows - 1) / kStepRows;
-    from = (int)((int64_t)blockIdx.y * steps / parts) * kStepRows;
-    to = std::min(M, (int)((int64_t)(blockIdx.y + 1) * steps / parts) * kStepRows);
+    const int steps = (M + ROWS - 1) / ROWS;
+    from = (int)((int64_t)blockIdx.y * steps / parts) * ROWS;
+    to = std::min(M, (int)((int64_t)(blockIdx.y + 1) * steps / parts) * ROWS);
   }
   const int k0 = tk * S, n0 = tn * S;
+  // a tile's columns of dy come in pieces of 8; one that reaches past the end of the row starts
+  // earlier (its columns are then computed twice, alike)
+  auto column = [&](int piece) {
+    const int n = n0 + 8 * piece;
+    return LOAD == kByElement || n + 8 <= N ? n : N - 8;
+  };
+  // 16-byte piece c of row m of a panel
+  auto place = [&](int m, int c) { return m * ROW + (c ^ (m % 4 * 4)) * 16; };
 
-  // this lane's columns 2 cp, 2 cp + 1 of the tile, rows 8 oct .. of a step; columns past the
-  // end read the last ones (their outputs are never stored)
-  const int oct = wave % 4, cp = wave / 4 * kWave + lane;
-  int kc = k0 + 2 * cp, nc = n0 + 2 * cp;
-  kc = kc < Kp ? kc : Kp - 2;
-  const int kb = (k0 + wave / 4 * kGroup < Kp ? k0 + wave / 4 * kGroup : Kp - kGroup) / kGroup;
-  if constexpr (VEC) nc = nc < N ? nc : N - 2;        // N even
-  const int na = nc < N ? nc : N - 1, nb = nc + 1 < N ? nc + 1 : N - 1;
-
-  constexpr int DW = DT == kF32 ? 2 : 1;              // words of two elements
-  uint32_t xr[8], dr[8][DW], sr = 0;                  // rows as loaded; lane i < 8: scale of row i
-  int tok = 0;                                        // lane i < 8: token of row i, a step ahead
+  // codes of this thread: rows mx + 32 p, columns 16 cx ..
+  const int mx = tid / (S / 16), cx = tid % (S / 16);
+  const int kc = k0 + 16 * cx < Kp ? k0 + 16 * cx : Kp - 16;   // past the end: never stored
+  const uint8_t* scol = sx + (int64_t)(kc / kGroup) * Ms;
+  // elements of dy: rows my + 16 p, piece cy
+  const int my = tid / (S / 8), cy = tid % (S / 8);
+  uint4 xr[PX];
+  uint32_t sr[PX];
+  int tok[PX];                                        // a step ahead of the codes
+  uint32_t yr[PY][WY];
   auto load_tok = [&](int m) {
     if constexpr (GR) {
-      const int r = m + 8 * oct + (lane & 7);
-      tok = clamp_route(rt.tok[r < to ? r : to - 1], 0, rt.T - 1);
-    }
-  };
-  auto load = [&](int m) {                            // rows m + 8 oct ..; past the end: the last
-    const int r = m + 8 * oct + (lane & 7);
-    const int64_t mine = GR ? tok : (r < to ? r : to - 1);
-    sr = sx[(int64_t)kb * Ms + mine];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int ri = m + 8 * oct + i < to ? m + 8 * oct + i : to - 1;
-      const int64_t src = GR ? __builtin_amdgcn_readlane(tok, i) : ri;
-      xr[i] = *reinterpret_cast<const uint16_t*>(qx + src * Kp + kc);
-      if constexpr (DT == kF32) {
-        const float* p = static_cast<const float*>(dy) + (int64_t)ri * ld;
-        if constexpr (VEC) {
-          const uint2 u = *reinterpret_cast<const uint2*>(p + nc);
-          dr[i][0] = u.x;
-          dr[i][DW - 1] = u.y;
-        } else {
-          dr[i][0] = __float_as_uint(p[na]);
-          dr[i][DW - 1] = __float_as_uint(p[nb]);
-        }
-      } else {
-        const uint16_t* p = static_cast<const uint16_t*>(dy) + (int64_t)ri * ld;
-        if constexpr (VEC) dr[i][0] = *reinterpret_cast<const uint32_t*>(p + nc);
-        else dr[i][0] = (uint32_t)p[na] | (uint32_t)p[nb] << 16;
+      for (int p = 0; p < PX; ++p) {
+        const int r = m + mx + 32 * p;
+        tok[p] = clamp_route(rt.tok[r < to ? r : to - 1], 0, rt.T - 1);
       }
     }
   };
-  auto put = [&](int m, uint8_t* X, uint8_t* Y) {     // the loaded rows (of step m) as operands
-    const int at = (oct * S + 2 * cp) * 16;
-    const int live = to - (m + 8 * oct);              // rows below the end
-    uint32_t w[8];
+  auto load = [&](int m) {                            // rows from m on; past the end: the last
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t byte = __builtin_amdgcn_readlane(sr, i);
-      const uint32_t c = byte == kF8NanByte ? 0x7F7Fu : xr[i];
-      const v2b v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)c, f8_scale(byte), false);
-      w[i] = i < live ? __builtin_bit_cast(uint32_t, v) : 0u;
+    for (int p = 0; p < PX; ++p) {
+      const int r = m + mx + 32 * p;
+      const int64_t src = GR ? tok[p] : (r < to ? r : to - 1);
+      xr[p] = *reinterpret_cast<const uint4*>(qx + src * Kp + kc);
+      sr[p] = scol[src];
     }
-    *reinterpret_cast<uint4*>(X + at) = make_uint4(low_halves(w[0], w[1]), low_halves(w[2], w[3]),
-                                                   low_halves(w[4], w[5]), low_halves(w[6], w[7]));
-    *reinterpret_cast<uint4*>(X + at + 16) =
-        make_uint4(high_halves(w[0], w[1]), high_halves(w[2], w[3]), high_halves(w[4], w[5]),
-                   high_halves(w[6], w[7]));
-    if constexpr (DT == kBF16) {
+    if constexpr (LOAD != kStraight) {
+      constexpr int B = DT == kF32 ? 4 : 2;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = i < live ? dr[i][0] : 0u;
-      *reinterpret_cast<uint4*>(Y + at) = make_uint4(low_halves(w[0], w[1]), low_halves(w[2], w[3]),
-                                                     low_halves(w[4], w[5]), low_halves(w[6], w[7]));
-      *reinterpret_cast<uint4*>(Y + at + 16) =
-          make_uint4(high_halves(w[0], w[1]), high_halves(w[2], w[3]), high_halves(w[4], w[5]),
-                     high_halves(w[6], w[7]));
-    } else {
+      for (int p = 0; p < PY; ++p) {
+        const int r = m + my + 16 * p;
+        const uint8_t* row = static_cast<const uint8_t*>(dy) + (int64_t)(r < to ? r : to - 1) * ld * B;
+        if constexpr (LOAD == kByPiece) {
+          __builtin_memcpy(yr[p], row + (int64_t)column(cy) * B, 8 * B);
+        } else {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {                   // the two columns
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if constexpr (DT == kF32) v[i] = __uint_as_float(dr[i][j]);
-          else {
-            const __half2 h = *reinterpret_cast<const __half2*>(&dr[i][0]);
-            v[i] = j == 0 ? __low2float(h) : __high2float(h);
+          for (int e = 0; e < 8; ++e) {
+            const int n = column(cy) + e < N ? column(cy) + e : N - 1;
+            if constexpr (DT == kF32) yr[p][e] = reinterpret_cast<const uint32_t*>(row)[n];
+            else {
+              const uint32_t h = reinterpret_cast<const uint16_t*>(row)[n];
+              yr[p][e / 2] = e % 2 ? yr[p][e / 2] | h << 16 : h;
+            }
           }
-          if (i >= live) v[i] = 0.0f;
         }
+      }
+    }
+  };
+  auto issue = [&](int m, uint8_t* Y) {               // rows from m on straight to the panel
+    if constexpr (LOAD == kStraight) {
 #pragma unroll
-        for (int t = 0; t < TERMS; ++t) {
+      for (int i = 0; i < PY; ++i) {
+        const int at = i * NW + wave;                 // 1 KiB each
+        const int r = at * (512 / S) + lane / (S / 8);
+        const int c = lane % (S / 8) ^ (r % 4 * 4);
+        const uint16_t* src = static_cast<const uint16_t*>(dy) + (int64_t)(m + r) * ld + column(c);
+        const void* p = m + r < to ? static_cast<const void*>(src) : &kZeroPiece;
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)p,
+                                         (__attribute__((address_space(3))) void*)(Y + at * 1024), 16, 0, 0);
+      }
+    }
+  };
+  auto put = [&](int m, uint8_t* X, uint8_t* Y) {     // the loaded rows (from m on) as operands
 #pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] = lead(v[i], v[i]);
-          *reinterpret_cast<uint4*>(Y + t * PANEL + at + 16 * j) =
-              make_uint4(high_halves(w[0], w[1]), high_halves(w[2], w[3]), high_halves(w[4], w[5]),
-                         high_halves(w[6], w[7]));
+    for (int p = 0; p < PX; ++p) {
+      const int r = mx + 32 * p;
+      const bool live = m + r < to;
+      const float scale = f8_scale(live ? sr[p] : 127u);
+      const uint32_t c[4] = {xr[p].x, xr[p].y, xr[p].z, xr[p].w};
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int q = live ? sr[p] == kF8NanByte ? 0x7F7F7F7F : (int)c[i] : 0;
+        w[2 * i] = __builtin_bit_cast(uint32_t, (v2b)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, scale, false));
+        w[2 * i + 1] = __builtin_bit_cast(uint32_t, (v2b)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, scale, true));
+      }
+      *reinterpret_cast<uint4*>(X + place(r, 2 * cx)) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(X + place(r, 2 * cx + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+    if constexpr (LOAD != kStraight) {
+#pragma unroll
+      for (int p = 0; p < PY; ++p) {
+        const int r = my + 16 * p;
+        const bool live = m + r < to;
+        uint8_t* out = Y + place(r, cy);
+        if constexpr (DT == kBF16) {
+          *reinterpret_cast<uint4*>(out) = live ? make_uint4(yr[p][0], yr[p][1], yr[p][2], yr[p][3])
+                                                : make_uint4(0, 0, 0, 0);
+        } else {
+          uint32_t w[TERMS][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float a, b;
+            if constexpr (DT == kF32) {
+              a = __uint_as_float(yr[p][2 * i]);
+              b = __uint_as_float(yr[p][2 * i + 1]);
+            } else {
+              const __half2 h = __builtin_bit_cast(__half2, yr[p][i]);
+              a = __low2float(h);
+              b = __high2float(h);
+            }
+            // a quiet NaN keeps its mark in the leading part; past an infinity nothing is left
+            a = live ? __builtin_canonicalizef(a) : 0.0f;
+            b = live ? __builtin_canonicalizef(b) : 0.0f;
+            const bool fa = __builtin_isfinite(a), fb = __builtin_isfinite(b);
+            w[0][i] = lead2(a, b);
+            a = fa ? a : 0.0f;
+            b = fb ? b : 0.0f;
+#pragma unroll
+            for (int t = 1; t < TERMS; ++t) w[t][i] = lead2(a, b);
+          }
+#pragma unroll
+          for (int t = 0; t < TERMS; ++t)
+            *reinterpret_cast<uint4*>(out + t * PANEL) = make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
         }
       }
     }
@@ -176,6 +211,22 @@ __global__ __launch_bounds__(S * 2) __attribute__((amdgpu_waves_per_eu(2))) void
 
   const int wk = wave / WN, wn = wave % WN;
   const int lr = lane % 32, hf = lane / 32;
+  // block b of 32 columns of a panel: this lane's place in its first four rows
+  auto corner = [&](int b) {
+    const int r = lane % 16 / 4, c = 2 * b + lane / 16 % 2;
+    return (8 * hf + r) * ROW + (c ^ (2 * r)) * 32 + lane % 4 * 8;
+  };
+  int ca[FK], cb[FN];
+#pragma unroll
+  for (int i = 0; i < FK; ++i) ca[i] = corner(wk * FK + i);
+#pragma unroll
+  for (int j = 0; j < FN; ++j) cb[j] = corner(wn * FN + j);
+  auto operand = [&](const uint8_t* P, int at) {      // eight rows of this lane's column
+    typedef __attribute__((address_space(3))) v4s* Ptr;
+    const v4s a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Ptr)(P + at));
+    const v4s b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Ptr)(P + at + 4 * ROW));
+    return __builtin_bit_cast(v8b, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
   v16f acc[FK][FN];
 #pragma unroll
   for (int i = 0; i < FK; ++i)
@@ -183,59 +234,124 @@ __global__ __launch_bounds__(S * 2) __attribute__((amdgpu_waves_per_eu(2))) void
     for (int j = 0; j < FN; ++j) acc[i][j] = v16f{0.0f};
   auto compute = [&](const uint8_t* X, const uint8_t* Y) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {                     // 16 rows each: pieces 2h + hf
+    for (int h = 0; h < ROWS / 16; ++h) {
       v8b a[FK];
 #pragma unroll
-      for (int i = 0; i < FK; ++i)
-        a[i] = *reinterpret_cast<const v8b*>(X + ((2 * h + hf) * S + wk * (S / 2) + 32 * i + lr) * 16);
+      for (int i = 0; i < FK; ++i) a[i] = operand(X, ca[i] + 16 * h * ROW);
 #pragma unroll
-      for (int t = TERMS - 1; t >= 0; --t)
+      for (int t = TERMS - 1; t >= 0; --t)            // the least term first
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-          const v8b b = *reinterpret_cast<const v8b*>(
-              Y + t * PANEL + ((2 * h + hf) * S + wn * (S / WN) + 32 * j + lr) * 16);
+          const v8b b = operand(Y, cb[j] + t * PANEL + 16 * h * ROW);
 #pragma unroll
           for (int i = 0; i < FK; ++i)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b, acc[i][j], 0, 0, 0);
+            acc[i][j] = DT == kF32 ? __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b, acc[i][j], 0, 0, 0)
+                                   : __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, a[i], acc[i][j], 0, 0, 0);
         }
     }
   };
   if (from < to) {
     load_tok(from);
     load(from);
-    load_tok(from + kStepRows);
+    load_tok(from + ROWS);
+    issue(from, Y0);
     put(from, X0, Y0);
-    load(from + kStepRows);
-    load_tok(from + 2 * kStepRows);
-    // stage of step m is written by all waves at the barrier, the other one is read
+    load(from + ROWS);
+    load_tok(from + 2 * ROWS);
     auto step = [&](int m, const uint8_t* X, const uint8_t* Y, uint8_t* Xn, uint8_t* Yn) {
-      __syncthreads();
-      put(m + kStepRows, Xn, Yn);
-      load(m + 2 * kStepRows);
-      load_tok(m + 3 * kStepRows);
+      if constexpr (LOAD == kStraight) wait_vm<0>();  // step m's rows of dy landed
+      wait_lds0();
+      lds_barrier();                                  // ... in every wave, and the others are read
+      issue(m + ROWS, Yn);
+      put(m + ROWS, Xn, Yn);
+      load(m + 2 * ROWS);
+      load_tok(m + 3 * ROWS);
       compute(X, Y);
     };
 #pragma unroll 1
-    for (int m = from; m < to; m += 2 * kStepRows) {
+    for (int m = from; m < to; m += 2 * ROWS) {
       step(m, X0, Y0, X1, Y1);
-      if (m + kStepRows < to) step(m + kStepRows, X1, Y1, X0, Y0);
+      if (m + ROWS < to) step(m + ROWS, X1, Y1, X0, Y0);
     }
+    if constexpr (LOAD == kStraight) wait_vm<0>();
   }
-  // lane: column n = lane % 32 of a block, rows k = 8 (r / 4) + 4 hf + r % 4
-#pragma unroll
-  for (int i = 0; i < FK; ++i)
+  float* const sums = !GR && parts > 1 ? part + (int64_t)blockIdx.y * K * N : nullptr;
+  if constexpr (DT == kF32) {
+    // lane: column n = lane % 32 of a block, rows k = 8 (r / 4) + 4 hf + r % 4
+    float* const y = sums ? sums : static_cast<float*>(dw.p) + out0;
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
-      const int n = n0 + wn * (S / WN) + 32 * j + lr;
+      const int pos = wn * 64 + 32 * j + lr, n = column(pos / 8) + pos % 8;
+      if (n0 + pos / 8 * 8 >= N || n >= N) continue;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int k = k0 + wk * (S / 2) + 32 * i + 8 * (r / 4) + 4 * hf + r % 4;
-        if (k >= K || n >= N) continue;
-        const int64_t o = (int64_t)k * N + n;
-        if (!GR && parts > 1) part[(int64_t)blockIdx.y * K * N + o] = acc[i][j][r];
-        else dw.put(out0 + o, acc[i][j][r]);
-      }
+      for (int i = 0; i < FK; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int k = k0 + wk * (S / 2) + 32 * i + 8 * (r / 4) + 4 * hf + r % 4;
+          if (k < K) y[(int64_t)k * N + n] = acc[i][j][r];
+        }
     }
+  } else if (sums) {
+    // lane: row k = lane % 32 of a block, columns n = 8 (r / 4) + 4 hf + r % 4
+#pragma unroll
+    for (int i = 0; i < FK; ++i) {
+      const int k = k0 + wk * (S / 2) + 32 * i + lr;
+      if (k >= K) continue;
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int piece = wn * 8 + 4 * j + q, n = column(piece) + 4 * hf;
+          if (n0 + 8 * piece >= N) continue;
+          float* o = sums + (int64_t)k * N + n;
+          const float v[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+          if constexpr (LOAD == kByElement) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (n + e < N) o[e] = v[e];
+          } else {
+            __builtin_memcpy(o, v, 16);
+          }
+        }
+    }
+  } else {
+    // through this wave's 4 KiB of LDS: 32 rows of 64 outputs, pieces swizzled by row
+    __syncthreads();                                  // every wave is done with the panels
+    uint8_t* const P = (wave % 4 == 0 ? X0 : wave % 4 == 1 ? X1 : wave % 4 == 2 ? Y0 : Y1) + wave / 4 * 4096;
+    static_assert(PANEL >= (NW + 3) / 4 * 4096, "a wave's part fits");
+    const bool vec = N % 8 == 0 && reinterpret_cast<uintptr_t>(dw.p) % 16 == 0;
+    uint16_t* const y = static_cast<uint16_t*>(dw.p) + out0;
+#pragma unroll
+    for (int i = 0; i < FK; ++i) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<uint2*>(P + lr * 128 + ((4 * j + q) ^ (lr % 8)) * 16 + 8 * hf) =
+              make_uint2(narrow2<DT>(acc[i][j][4 * q], acc[i][j][4 * q + 1]),
+                         narrow2<DT>(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]));
+      wait_lds0();
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int row = 8 * t + lane / 8, c = lane % 8;
+        const uint4 v = *reinterpret_cast<const uint4*>(P + row * 128 + (c ^ (row % 8)) * 16);
+        const int k = k0 + wk * (S / 2) + 32 * i + row, n = column(wn * 8 + c);
+        if (k >= K || n0 + 8 * (wn * 8 + c) >= N) continue;
+        uint16_t* o = y + (int64_t)k * N + n;
+        if (vec) {
+          *reinterpret_cast<uint4*>(o) = v;
+        } else {
+          const uint16_t* e = reinterpret_cast<const uint16_t*>(&v);
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            if (n + u < N) o[u] = e[u];
+        }
+      }
+      wait_lds0();
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
 }
 
 // the parts' sums, in order
@@ -269,14 +385,15 @@ hipError_t wgrad_t(const uint8_t* qx, const uint8_t* sx, const void* dy, int64_t
   const dim3 grid((unsigned)tiles, (unsigned)(GR ? rt.E : parts)), block(kTile * 2);
   if (!grid_fits(tiles, kTile * 2) || !grid_fits((K * N + 255) / 256, 256))
     return hipErrorInvalidConfiguration;
-  constexpr int two = DT == kF32 ? 8 : 4;             // bytes of two elements of dy
-  const bool vec = N % 2 == 0 && ld % 2 == 0 && reinterpret_cast<uintptr_t>(dy) % two == 0;
-  if (vec)
-    hipLaunchKernelGGL((k_f8_wgrad<kTile, DT, true, GR>), grid, block, 0, stream, qx, sx, dy, ld,
-                       (int)M, (int)K, (int)N, rt, dw, parts, ws);
-  else
-    hipLaunchKernelGGL((k_f8_wgrad<kTile, DT, false, GR>), grid, block, 0, stream, qx, sx, dy, ld,
-                       (int)M, (int)K, (int)N, rt, dw, parts, ws);
+  const bool aligned = DT == kBF16 && N % 8 == 0 && ld % 8 == 0 && reinterpret_cast<uintptr_t>(dy) % 16 == 0;
+#define BGT_CALL(LOAD)                                                                              \
+  hipLaunchKernelGGL((k_f8_wgrad<kTile, DT == kBF16 ? 64 : 32, DT, LOAD, GR>), grid, block, 0, stream, qx, sx, \
+                     dy, ld, (int)M, (int)K, (int)N, rt, dw, parts, ws)
+  if constexpr (DT == kBF16)
+    if (aligned) BGT_CALL(kStraight);
+  if (!aligned && N >= 8) BGT_CALL(kByPiece);
+  if (N < 8) BGT_CALL(kByElement);
+#undef BGT_CALL
   if (parts > 1)
     hipLaunchKernelGGL(k_f8_wgrad_join, dim3((unsigned)((K * N + 255) / 256)), dim3(256), 0, stream,
                        ws, parts, K * N, dw);
