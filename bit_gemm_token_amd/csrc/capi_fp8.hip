@@ -105,7 +105,7 @@ int bgt_w8a8_moe_gemm_fp8(const uint8_t* qx, const uint8_t* sx, int64_t T,
 
 int64_t bgt_wgrad_fp8_workspace_bytes(int64_t M, int64_t K, int64_t N) {
   if (!rows_ok(M, K) || N < 1 || N > kMaxCols) return BGT_ERR_SHAPE;
-  return bgt::f8_wgrad_ws_bytes(M, K, N, 0);
+  return bgt::f8_wgrad_ws_bytes(M, K, N);
 }
 
 int bgt_wgrad_fp8(const uint8_t* qx, const uint8_t* sx, const void* dy, int type, int64_t lddy,
@@ -114,7 +114,7 @@ int bgt_wgrad_fp8(const uint8_t* qx, const uint8_t* sx, const void* dy, int type
   if (!qx || !sx || !dy || !dw) return BGT_ERR_NULL;
   if (!valid_type(type)) return BGT_ERR_MODE;
   if (!rows_ok(M, K) || N < 1 || N > kMaxCols || lddy < N) return BGT_ERR_SHAPE;
-  const int64_t need = bgt::f8_wgrad_ws_bytes(M, K, N, 0);
+  const int64_t need = bgt::f8_wgrad_ws_bytes(M, K, N);
   if (need > 0 && !ws) return BGT_ERR_NULL;
   if (ws_bytes < need) return BGT_ERR_SHAPE;
   const int b = type_bytes(type);

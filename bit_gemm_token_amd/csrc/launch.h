@@ -172,7 +172,7 @@ hipError_t launch_w8a8_f8_linear(const void* x, int type, int64_t ldx, int64_t K
                                  const uint8_t* sw, int64_t M, int64_t N, int64_t K, uint8_t* q,
                                  uint8_t* s, OutY y, hipStream_t stream);
 // dw = values(qx)^T dy for one matrix (rt.E == 0) or each expert of a route; ws: fp32 parts
-int64_t f8_wgrad_ws_bytes(int64_t M, int64_t K, int64_t N, int64_t E);
+int64_t f8_wgrad_ws_bytes(int64_t M, int64_t K, int64_t N);
 hipError_t launch_f8_wgrad(const uint8_t* qx, const uint8_t* sx, const void* dy, int64_t ld,
                            int64_t M, int64_t K, int64_t N, const Route& rt, OutY dw, void* ws,
                            hipStream_t stream);
