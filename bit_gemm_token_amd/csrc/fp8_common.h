@@ -23,10 +23,6 @@ __device__ __forceinline__ uint32_t f8_scale_byte(uint32_t top) {
   const int b = (int)((top + 0x1FFFFFu) >> 23) - 8;
   return b < (int)kF8MinByte ? kF8MinByte : (uint32_t)b;
 }
-// 2^(127 - byte), the factor from values to codes; NaN for the NaN byte
-__device__ __forceinline__ float f8_inverse(uint32_t byte) {
-  return __uint_as_float(byte == kF8NanByte ? 0x7FC00000u : (254u - byte) << 23);
-}
 // 2^(byte - 127) (byte 0 is a subnormal); NaN for the NaN byte
 __device__ __forceinline__ float f8_scale(uint32_t byte) {
   return __uint_as_float(byte == kF8NanByte ? 0x7FC00000u : byte == 0 ? 0x00400000u : byte << 23);
@@ -34,10 +30,21 @@ __device__ __forceinline__ float f8_scale(uint32_t byte) {
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
-// four values to four codes (round to nearest even), first value in the low byte
-__device__ __forceinline__ uint32_t f8_pack4(float a, float b, float c, float d) {
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+// the largest over a row of 16 lanes, in all of them: lane exchanges of the vector unit (pairs,
+// quads, then the row's halves mirrored)
+__device__ __forceinline__ uint32_t max16(uint32_t t) {
+  t = umax(t, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)t, 0xB1, 0xF, 0xF, true));
+  t = umax(t, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)t, 0x4E, 0xF, 0xF, true));
+  t = umax(t, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)t, 0x141, 0xF, 0xF, true));
+  return umax(t, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)t, 0x140, 0xF, 0xF, true));
+}
+
+// four values over scale (a power of two) to four codes, rounded once to nearest even, first
+// value in the low byte; whatever of a block whose scale is NaN
+__device__ __forceinline__ uint32_t f8_pack4(float a, float b, float c, float d, float scale) {
+  typedef short v2s __attribute__((ext_vector_type(2)));
+  v2s w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(v2s{0, 0}, a, b, scale, false);
+  return __builtin_bit_cast(uint32_t, (v2s)__builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, c, d, scale, true));
 }
 // the four codes of a word as values
 __device__ __forceinline__ void f8_unpack4(uint32_t w, float* v) {

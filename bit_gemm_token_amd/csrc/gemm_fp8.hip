@@ -271,12 +271,10 @@ __global__ __launch_bounds__(stream_waves(MT, CH) * 64) void k_f8_stream(
             uint32_t top = 0;
 #pragma unroll
             for (int u = 0; u < 8; ++u) top = umax(top, abs_bits(v[u]));
-#pragma unroll
-            for (int o = 1; o < 16; o <<= 1) top = umax(top, (uint32_t)__shfl_xor((int)top, o, kWave));
-            byte = f8_scale_byte(top);
-            const float inv = f8_inverse(byte);
-            q.x = f8_pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-            q.y = f8_pack4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+            byte = f8_scale_byte(max16(top));
+            const float scale = f8_scale(byte);
+            q.x = f8_pack4(v[0], v[1], v[2], v[3], scale);
+            q.y = f8_pack4(v[4], v[5], v[6], v[7], scale);
             if (write && row < M && g < G) {
               *reinterpret_cast<uint2*>(q_out + (int64_t)row * K + k) = q;
               if (c == 0) s_out[(int64_t)g * M + row] = (uint8_t)byte;

@@ -25,13 +25,10 @@ __device__ __forceinline__ uint32_t top_of(const float* v) {
   uint32_t t = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) t = umax(t, abs_bits(v[j]));
-#pragma unroll
-  for (int o = 1; o < kRowLanes; o <<= 1) t = umax(t, (uint32_t)__shfl_xor((int)t, o, kWave));
-  return t;
+  return max16(t);
 }
-__device__ __forceinline__ uint2 codes_of(const float* v, float inv) {
-  return make_uint2(f8_pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
-                    f8_pack4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+__device__ __forceinline__ uint2 codes_of(const float* v, float scale) {
+  return make_uint2(f8_pack4(v[0], v[1], v[2], v[3], scale), f8_pack4(v[4], v[5], v[6], v[7], scale));
 }
 template <int IT, bool VEC>
 __device__ __forceinline__ void load_piece(const void* x, int64_t row, int c, int K, float* v) {
@@ -67,7 +64,7 @@ __global__ __launch_bounds__(kThreads) void k_f8_rows(const void* __restrict__ x
     const int64_t m = m0 + s * kRowsAtOnce;
     const uint32_t byte = f8_scale_byte(top_of(v[s]));
     if (m >= M) continue;
-    *reinterpret_cast<uint2*>(q + m * ((int64_t)G * kGroup) + c) = codes_of(v[s], f8_inverse(byte));
+    *reinterpret_cast<uint2*>(q + m * ((int64_t)G * kGroup) + c) = codes_of(v[s], f8_scale(byte));
     if (threadIdx.x % kRowLanes == 0) scale[(int64_t)b * M + m] = (uint8_t)byte;
   }
 }
@@ -153,13 +150,14 @@ __global__ __launch_bounds__(256) void k_f8_weights(const void* __restrict__ w, 
   for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) top = umax(top, abs_bits(v[i][j]));
+  top = max16(top);
 #pragma unroll
-  for (int o = 1; o < kWave; o <<= 1) top = umax(top, (uint32_t)__shfl_xor((int)top, o, kWave));
+  for (int o = kRowLanes; o < kWave; o <<= 1) top = umax(top, (uint32_t)__shfl_xor((int)top, o, kWave));
   if (t % kWave == 0) tops[t / kWave] = top;
   __syncthreads();
   top = umax(umax(tops[0], tops[1]), umax(tops[2], tops[3]));
   const uint32_t byte = f8_scale_byte(top);
-  const float inv = f8_inverse(byte);
+  const float scale = f8_scale(byte);
   if (t == 0) {
     sw[(e * A + a) * B + b] = (uint8_t)byte;
     if (st != nullptr) st[(e * B + b) * A + a] = (uint8_t)byte;
@@ -167,7 +165,7 @@ __global__ __launch_bounds__(256) void k_f8_weights(const void* __restrict__ w, 
   uint32_t lo[8], hi[8];                             // row i: columns 0..3 and 4..7
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint2 c = codes_of(v[i], inv);
+    const uint2 c = codes_of(v[i], scale);
     lo[i] = c.x;
     hi[i] = c.y;
   }
@@ -198,8 +196,28 @@ __global__ __launch_bounds__(256) void k_f8_weights(const void* __restrict__ w, 
 }
 
 // --------------------------------------------------------------------- gated activation
-// 1 / (1 + exp(-g)): exp(-g) overflows to infinity for g < -88.7 and the quotient is 0
-__device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + expf(-g)); }
+// 1 / (1 + exp(-g)) from t = exp(-|g|), which does not overflow: 1 / (1 + t), for g < 0 times t.
+// t = 2^y (1 + r ln 2) with y + r = -|g| log2(e) to twice fp32's digits; 1 + t lies in [1, 2], where
+// the reciprocal instruction is right to one unit. (8192 x 14336 bf16: 200 us with expf and a division,
+// which instructions bound, VARIANT so.) A NaN gives 1; every use multiplies by g too.
+__device__ __forceinline__ float sigmoid(float g) {
+  const float a = -fminf(fabsf(g), 200.0f);           // t is 0 from 104 on
+  const float y = a * 1.44269504f;
+  const float r = __builtin_fmaf(a, 1.92596299e-8f, __builtin_fmaf(a, 1.44269504f, -y));
+  const float e = __builtin_exp2f(y), t = __builtin_fmaf(e, r * 0.693147181f, e);
+  const float s = __builtin_amdgcn_rcpf(1.0f + t);
+  return g < 0.0f ? t * s : s;
+}
+
+// The same where the result goes to 8 bits: below 2^-126 (g < -87) it may be 0. 1 / (1 + t) with
+// t = exp(-g), infinite where that overflows.
+__device__ __forceinline__ float sigmoid_fast(float g) {
+  const float a = __builtin_amdgcn_fmed3f(-g, -100.0f, 100.0f);
+  const float y = a * 1.44269504f;
+  const float r = __builtin_fmaf(a, 1.92596299e-8f, __builtin_fmaf(a, 1.44269504f, -y));
+  const float t = __builtin_amdgcn_exp2f(y) * __builtin_fmaf(r, 0.693147181f, 1.0f);
+  return __builtin_amdgcn_rcpf(1.0f + t);
+}
 
 template <int IT, bool VEC, int STEPS>
 __global__ __launch_bounds__(kThreads) void k_f8_gate(
@@ -222,14 +240,18 @@ __global__ __launch_bounds__(kThreads) void k_f8_gate(
     const int64_t m = m0 + s * kRowsAtOnce;
     float h[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) h[j] = g[s][j] * sigmoid(g[s][j]) * u[s][j];
-    const uint32_t bh = f8_scale_byte(top_of(h)), bg = f8_scale_byte(top_of(g[s]));
-    const uint32_t bu = f8_scale_byte(top_of(u[s]));
+    for (int j = 0; j < 8; ++j) h[j] = g[s][j] * sigmoid_fast(g[s][j]) * u[s][j];
+    const uint32_t bg = f8_scale_byte(top_of(g[s])), bu = f8_scale_byte(top_of(u[s]));
+    float top = 0.0f;                                 // a NaN of h comes from one, or an infinity, of g or u
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(h[j]));
+    uint32_t bh = f8_scale_byte(max16(__float_as_uint(top)));
+    bh = umax(bh, umax(bg, bu) == kF8NanByte ? kF8NanByte : 0u);
     if (m >= M) continue;
     const int64_t o = m * ((int64_t)G * kGroup) + c;
-    *reinterpret_cast<uint2*>(hq + o) = codes_of(h, f8_inverse(bh));
-    *reinterpret_cast<uint2*>(gq + o) = codes_of(g[s], f8_inverse(bg));
-    *reinterpret_cast<uint2*>(uq + o) = codes_of(u[s], f8_inverse(bu));
+    *reinterpret_cast<uint2*>(hq + o) = codes_of(h, f8_scale(bh));
+    *reinterpret_cast<uint2*>(gq + o) = codes_of(g[s], f8_scale(bg));
+    *reinterpret_cast<uint2*>(uq + o) = codes_of(u[s], f8_scale(bu));
     if (threadIdx.x % kRowLanes == 0) {
       hs[(int64_t)b * M + m] = (uint8_t)bh;
       gs[(int64_t)b * M + m] = (uint8_t)bg;
