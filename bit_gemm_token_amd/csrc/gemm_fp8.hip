@@ -378,6 +378,9 @@ __global__ __launch_bounds__(stream_waves(MT, CH) * 64) void k_f8_stream(
   if (late >= 0) y.put(late, value);
 }
 
+template <bool B, class T, class F> struct Pick { using type = T; };
+template <class T, class F> struct Pick<false, T, F> { using type = F; };
+
 // =====================================================================
 // Many rows: BN x BM output tiles through LDS
 // =====================================================================
@@ -387,6 +390,12 @@ __global__ __launch_bounds__(stream_waves(MT, CH) * 64) void k_f8_stream(
 // (16-byte pieces XOR-swizzled by row, so that the 32 rows of an operand read fall on
 // distinct banks), two stages, one barrier a step. 16-bit outputs leave through the stages'
 // LDS as whole rows.
+//
+// The 256 x 256 tile reads the operands of 64 k while those of the 64 before them are multiplied
+// (two sets of registers), so that a group's two LDS reads and its copies run under the products;
+// its copies are 32-bit offsets from one base in scalar registers, for want of vector registers
+// (8192 x 14336 into 4096: 391 us, 425 without; 8192^3 467 and 474). Smaller tiles lose by it
+// (128 x 128, 8192^3: 576 and 532): more workgroups a CU do the same for them.
 template <int BN, int BM, int WN, int WM, bool EX, bool GR>
 __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(2))) void k_f8_tile(
     const uint8_t* __restrict__ qx, const uint8_t* __restrict__ sx, const uint8_t* __restrict__ qw,
@@ -428,40 +437,53 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(2)
 
   // copy i of this wave: rows 8 b .. 8 b + 7, b = NW i + wave; lane L fills row 8 b + L / 8,
   // slot L % 8 with the row's piece (L % 8) ^ ((row / 2) % 8)
-  const uint8_t *wsrc[WCP], *xsrc[XCP];
+  constexpr bool HALVES = BN == 256;
+  const uint8_t* const wbase = qw + (int64_t)n0 * K;
+  const uint8_t* const xbase = qx + (GR ? 0 : (int64_t)m0 * K);
+  typename Pick<HALVES, uint32_t, int64_t>::type wofs[WCP], xofs[XCP];   // a CU's rows, or T x K, below 2^32
 #pragma unroll
   for (int i = 0; i < WCP; ++i) {
     const int r = 8 * (NW * i + wave) + lane / 8;
-    wsrc[i] = qw + (int64_t)(n0 + r < N ? n0 + r : N - 1) * K + 16 * ((lane % 8) ^ ((r >> 1) & 7));
+    wofs[i] = (int64_t)(n0 + r < N ? r : N - 1 - n0) * K + 16 * ((lane % 8) ^ ((r >> 1) & 7));
   }
 #pragma unroll
   for (int i = 0; i < XCP; ++i) {
     const int r = 8 * (NW * i + wave) + lane / 8;
-    xsrc[i] = qx + source_row(r) * K + 16 * ((lane % 8) ^ ((r >> 1) & 7));
+    xofs[i] = (source_row(r) - (GR ? 0 : m0)) * K + 16 * ((lane % 8) ^ ((r >> 1) & 7));
   }
+  auto copy = [&](const uint8_t* base, auto ofs, int g, uint8_t* to) {   // 1 KiB a wave
+    auto* const l = (__attribute__((address_space(3))) void*)to;
+    if constexpr (HALVES)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, -1, 0x27000), l, 16, (int)ofs,
+          g * kGroup, 0, 0);
+    else
+      __builtin_amdgcn_global_load_lds(
+          (const __attribute__((address_space(1))) void*)(base + ofs + (int64_t)g * kGroup), l, 16, 0, 0);
+  };
   auto issue = [&](int g, uint8_t* S) {
 #pragma unroll
-    for (int i = 0; i < WCP; ++i)
-      __builtin_amdgcn_global_load_lds(
-          (const __attribute__((address_space(1))) void*)(wsrc[i] + (int64_t)g * kGroup),
-          (__attribute__((address_space(3))) void*)(S + (NW * i + wave) * 1024), 16, 0, 0);
+    for (int i = 0; i < WCP; ++i) copy(wbase, wofs[i], g, S + (NW * i + wave) * 1024);
 #pragma unroll
-    for (int i = 0; i < XCP; ++i)
-      __builtin_amdgcn_global_load_lds(
-          (const __attribute__((address_space(1))) void*)(xsrc[i] + (int64_t)g * kGroup),
-          (__attribute__((address_space(3))) void*)(S + BN * kGroup + (NW * i + wave) * 1024), 16, 0, 0);
+    for (int i = 0; i < XCP; ++i) copy(xbase, xofs[i], g, S + BN * kGroup + (NW * i + wave) * 1024);
   };
   const int64_t Ms = GR ? rt.T : M;
-  const uint8_t* ssrc[FM];
+  int ssrc[FM];
 #pragma unroll
-  for (int i = 0; i < FM; ++i) ssrc[i] = sx + source_row(wm * (BM / WM) + 32 * i + lr);
+  for (int i = 0; i < FM; ++i) ssrc[i] = (int)source_row(wm * (BM / WM) + 32 * i + lr);
   const int nb = (n0 + wn * (BN / WN)) / kGroup;
   const uint8_t* wscale = sw + (nb < B ? nb : B - 1);
   uint32_t sa[FM], sb, na[FM], nb1;
   auto scales = [&](int g) {
     nb1 = wscale[(int64_t)g * B];
+    const uint8_t* const sg = sx + (int64_t)g * Ms;
 #pragma unroll
-    for (int i = 0; i < FM; ++i) na[i] = ssrc[i][(int64_t)g * Ms];
+    for (int i = 0; i < FM; ++i) na[i] = sg[ssrc[i]];
+  };
+  auto take_scales = [&] {
+    sb = nb1;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) sa[i] = na[i];
   };
 
   auto fragment = [&](const uint8_t* S, int r, int h) {       // 32 codes: pieces 4h + 2hf, + 1
@@ -475,61 +497,98 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(2)
   for (int i = 0; i < FN; ++i)
 #pragma unroll
     for (int m = 0; m < FM; ++m) acc[i][m] = v16f{0.0f};
-  auto compute = [&](const uint8_t* S) {
-    if constexpr (EX) {
+  auto read = [&](const uint8_t* S, int h, v8i* w, v8i* xx) {  // operands of 64 k
 #pragma unroll
-      for (int i = 0; i < FN; ++i)
+    for (int i = 0; i < FN; ++i) w[i] = fragment(S, wn * (BN / WN) + 32 * i + lr, h);
 #pragma unroll
-        for (int m = 0; m < FM; ++m) {
-          v16f p = v16f{0.0f};
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const v8i w = fragment(S, wn * (BN / WN) + 32 * i + lr, h);
-            const v8i xx = fragment(S + BN * kGroup, wm * (BM / WM) + 32 * m + lr, h);
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              p = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen8(w, u), widen8(xx, u), p, 0, 0, 0);
-          }
-          const float a = f8_scale(sa[m]), b = f8_scale(sb);
-#pragma unroll
-          for (int r = 0; r < 16; ++r) acc[i][m][r] = acc[i][m][r] + p[r] * a * b;
-        }
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        v8i w[FN], xx[FM];
-#pragma unroll
-        for (int i = 0; i < FN; ++i) w[i] = fragment(S, wn * (BN / WN) + 32 * i + lr, h);
-#pragma unroll
-        for (int m = 0; m < FM; ++m) xx[m] = fragment(S + BN * kGroup, wm * (BM / WM) + 32 * m + lr, h);
-#pragma unroll
-        for (int i = 0; i < FN; ++i)
-#pragma unroll
-          for (int m = 0; m < FM; ++m)
-            acc[i][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w[i], xx[m], acc[i][m], 0, 0, 0,
-                                                                        (int)sb, 0, (int)sa[m]);
-      }
-    }
+    for (int m = 0; m < FM; ++m) xx[m] = fragment(S + BN * kGroup, wm * (BM / WM) + 32 * m + lr, h);
   };
-  auto step = [&](int g, uint8_t* cur, uint8_t* nxt) {
-    wait_vm<0>();                                     // group g and its scales landed
-    lds_barrier();                                    // ... in every wave, and nxt is read
-    sb = nb1;
+  auto multiply = [&](const v8i* w, const v8i* xx) {
 #pragma unroll
-    for (int i = 0; i < FM; ++i) sa[i] = na[i];
-    if (g + 1 < G) {
-      scales(g + 1);
-      issue(g + 1, nxt);
-    }
-    compute(cur);
-    wait_lds0();
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int m = 0; m < FM; ++m)
+        acc[i][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w[i], xx[m], acc[i][m], 0, 0, 0,
+                                                                    (int)sb, 0, (int)sa[m]);
   };
   scales(0);
   issue(0, S0);
+  if constexpr (HALVES) {
+    v8i wa[FN], xa[FM], wb[FN], xb[FM];
+    auto step = [&](int g, uint8_t* cur, uint8_t* nxt) {
+      take_scales();
+      scales(g + 1 < G ? g + 1 : G - 1);
+      read(cur, 1, wb, xb);
+      multiply(wa, xa);
+      __builtin_amdgcn_sched_barrier(0);
+      wait_lds0();                                    // cur is read, and group g + 1 landed
+      wait_vm<0>();
+      asm volatile("" ::: "memory");
+      lds_barrier();                                  // ... in every wave
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      issue(g + 2 < G ? g + 2 : G - 1, cur);          // past the end: never read
+      read(nxt, 0, wa, xa);
+      multiply(wb, xb);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    issue(G > 1 ? 1 : 0, S1);
+    wait_vm<0>();
+    asm volatile("" ::: "memory");
+    lds_barrier();
+    asm volatile("" ::: "memory");
+    read(S0, 0, wa, xa);
 #pragma unroll 1
-  for (int g = 0; g < G; g += 2) {
-    step(g, S0, S1);
-    if (g + 1 < G) step(g + 1, S1, S0);
+    for (int g = 0; g < G; g += 2) {
+      step(g, S0, S1);
+      if (g + 1 < G) step(g + 1, S1, S0);
+    }
+    wait_vm<0>();
+  } else {
+    auto compute = [&](const uint8_t* S) {
+      if constexpr (EX) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+          for (int m = 0; m < FM; ++m) {
+            v16f p = v16f{0.0f};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const v8i w = fragment(S, wn * (BN / WN) + 32 * i + lr, h);
+              const v8i xx = fragment(S + BN * kGroup, wm * (BM / WM) + 32 * m + lr, h);
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                p = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen8(w, u), widen8(xx, u), p, 0, 0, 0);
+            }
+            const float a = f8_scale(sa[m]), b = f8_scale(sb);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][m][r] = acc[i][m][r] + p[r] * a * b;
+          }
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          v8i w[FN], xx[FM];
+          read(S, h, w, xx);
+          multiply(w, xx);
+        }
+      }
+    };
+    auto step = [&](int g, uint8_t* cur, uint8_t* nxt) {
+      wait_vm<0>();                                   // group g and its scales landed
+      lds_barrier();                                  // ... in every wave, and nxt is read
+      take_scales();
+      if (g + 1 < G) {
+        scales(g + 1);
+        issue(g + 1, nxt);
+      }
+      compute(cur);
+      wait_lds0();
+    };
+#pragma unroll 1
+    for (int g = 0; g < G; g += 2) {
+      step(g, S0, S1);
+      if (g + 1 < G) step(g + 1, S1, S0);
+    }
   }
 
   if constexpr (EX) {                                 // fp32: runs of four outputs a lane
@@ -677,7 +736,8 @@ hipError_t launch_t(const uint8_t* qx, const uint8_t* sx, const uint8_t* qw, con
     return rows * ((N + t - 1) / t);
   };
   const int64_t busy = (int64_t)device_cus() * 4 / 5;
-  if (tiles(256) >= busy && per >= 256)
+  const bool near = !GR || (int64_t)rt.T * K < (1LL << 32);    // rows of x within 32-bit offsets
+  if (tiles(256) >= busy && per >= 256 && near)
     return tile_t<256, 256, 4, 2, false, GR>(qx, sx, qw, sw, M, N, K, y, rt, stream);
   if (tiles(128) >= busy)
     return tile_t<128, 128, 2, 2, false, GR>(qx, sx, qw, sw, M, N, K, y, rt, stream);
