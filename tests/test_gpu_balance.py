@@ -136,3 +136,20 @@ def test_parts_of_a_batch_add_up(bgt, dev):
     d = torch.ones((), device=dev)
     both = torch.cat([bgt.moe_balance_backward(d, logits[a:b], counts, tokens) for a, b in ((0, 300), (300, 900))])
     assert torch.equal(both, bgt.moe_balance_backward(d, logits, whole[1], whole[3]))
+
+
+def test_two_streams(bgt, dev):
+    """Equal bits on two streams at once, with workspaces of their own."""
+    cases = [inputs(T, T, E, 2, 0.1, dev, torch.bfloat16) for T, E in ((5000, 64), (61, 8), (2000, 256))]
+    ref = [bgt.moe_balance(*c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        got = []
+        for st in streams:
+            with torch.cuda.stream(st):
+                got.append([bgt.moe_balance(*c) for c in cases])
+        torch.cuda.synchronize()
+        for out in got:
+            for a, b in zip(out, ref):
+                assert all(torch.equal(u, v) for u, v in zip(a, b))

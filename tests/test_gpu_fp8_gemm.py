@@ -84,9 +84,28 @@ def test_linear(bgt, dev, xtype, M, K, N):
     assert bgt.w8a8_linear_fp8(x, p["qw"], p["sw"])[0].dtype == xtype
 
 
+# few rows: more blocks of 16 weight rows than workgroups, K longer than the waves keep, each
+# count of row blocks; many rows: every tile with one, two and three groups of K and ragged ends
+WIDE = [(1, 4096, 9000), (9, 4096, 4400), (17, 4096, 4400), (48, 2048, 6000), (64, 4096, 4400), (1, 5120, 48), (8, 14336, 40),
+        (16, 8192, 64), (33, 4224, 40), (61, 14336, 100), (1024, 128, 14336), (1100, 256, 12300), (1030, 300, 12345),
+        (1000, 128, 3500), (1000, 200, 3500), (999, 384, 3501), (130, 5000, 1000), (66, 128, 70), (4000, 640, 3333)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,K,N", WIDE)
+def test_wide(bgt, dev, dtype, M, K, N):
+    print("wide", M, K, N, dtype, flush=True)
+    x, w = inputs(M + K + N, M, K, N, dev)
+    q, s = bgt.quantize_fp8(x)
+    p = bgt.pack_weights_fp8(w)
+    y = torch.full((M, N), float("nan"), device=dev, dtype=dtype)
+    check(bgt.w8a8_gemm_fp8(q, s, p["qw"], p["sw"], y=y), plain.values(q, s), plain.matrix(p["qw"], p["sw"]), dtype)
+
+
 ROUTED = [(1, 8, 2, 0.0, 512, 256), (3, 4, 1, 0.0, 128, 100), (16, 8, 2, 0.0, 1024, 512), (61, 5, 3, 0.2, 384, 129),
           (100, 3, 2, 0.5, 130, 64), (300, 4, 2, 0.1, 256, 272), (1000, 2, 1, 0.0, 512, 300), (700, 64, 4, 0.1, 256, 96),
-          (9, 4, 2, 1.0, 256, 64)]
+          (9, 4, 2, 1.0, 256, 64), (20, 4, 2, 0.0, 5000, 200), (40, 8, 2, 0.1, 1024, 4400), (1500, 2, 1, 0.1, 128, 10000),
+          (1600, 2, 1, 0.0, 384, 10001), (400, 4, 2, 0.1, 256, 3400), (3, 4, 2, 0.0, 8192, 48)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -176,6 +195,24 @@ def test_many_elements(bgt, dev):
     y = bgt.w8a8_gemm_fp8(q, s, p["qw"], p["sw"], out_dtype=torch.bfloat16)
     check(y[-80:], plain.values(a, b), plain.matrix(p["qw"], p["sw"]), torch.bfloat16)
     assert not bool(y[:1000].any()) and not bool(y[-180:-80].any())
+
+
+@pytest.mark.parametrize("more", [18, 19])
+def test_many_routed_elements(bgt, dev, more):
+    """Codes of routed rows past 2^31 and past 2^32 bytes."""
+    T, K, N = (1 << more) + 70, 8192, 256
+    q = torch.zeros(T, K, device=dev, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    s = torch.full((K // 128, T), 127, device=dev, dtype=torch.uint8).view(torch.float8_e8m0fnu)
+    x, w = inputs(more, 80, K, N, dev, 2)
+    a, b = bgt.quantize_fp8(x)
+    q[-80:].view(torch.uint8).copy_(a.view(torch.uint8))
+    s.view(torch.uint8)[:, -80:].copy_(b.view(torch.uint8))
+    p = bgt.pack_weights_fp8(w)
+    offs = torch.tensor([0, T // 2, T], dtype=torch.int32, device=dev)
+    tok = torch.arange(T, dtype=torch.int32, device=dev)
+    y = bgt.w8a8_moe_gemm_fp8(q, s, offs, tok, p["qw"], p["sw"], out_dtype=torch.bfloat16)
+    check(y[-80:], plain.values(a, b), plain.matrix(p["qw"][1], p["sw"][1]), torch.bfloat16)
+    assert not bool(y[:-80].any())
 
 
 def test_refusals(bgt, dev):

@@ -47,7 +47,8 @@ def check(dw, x, dy):
 
 
 SHAPES = [(1, 1, 1), (1, 128, 256), (5, 130, 77), (31, 300, 256), (32, 256, 257), (33, 1000, 130), (64, 513, 512), (100, 128, 128),
-          (257, 384, 640), (1000, 256, 256), (1021, 272, 258), (4096, 512, 300), (3000, 1408, 1024)]
+          (257, 384, 640), (1000, 256, 256), (1021, 272, 258), (4096, 512, 300), (3000, 1408, 1024),
+          (600, 3000, 4200), (600, 3000, 4203), (130, 3000, 4200), (300, 256, 3), (2100, 130, 7), (2500, 130, 77), (520, 4100, 8)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -72,7 +73,8 @@ def test_strides(bgt, dev, dtype):
 
 
 ROUTED = [(1, 8, 2, 0.0, 128, 256), (7, 4, 1, 0.3, 130, 77), (61, 8, 2, 0.0, 512, 256), (300, 5, 3, 0.2, 256, 300),
-          (1000, 32, 4, 0.1, 264, 128), (9, 4, 2, 1.0, 256, 64), (700, 2, 2, 0.0, 384, 129)]
+          (1000, 32, 4, 0.1, 264, 128), (9, 4, 2, 1.0, 256, 64), (700, 2, 2, 0.0, 384, 129),
+          (1100, 2, 1, 0.0, 2600, 2600), (1200, 2, 1, 0.1, 2600, 2601), (50, 4, 2, 0.1, 130, 5), (900, 32, 4, 0.1, 1024, 264)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -89,6 +91,26 @@ def test_routed(bgt, dev, dtype, T, E, k, drop, K, N):
     for e in range(E):
         a, b = int(offs[e]), int(offs[e + 1])
         check(dw[e], v[tok[a:b].long()], dy[a:b])
+
+
+def test_two_streams(bgt, dev):
+    """Equal bits on two streams at once, with workspaces (parts of the rows) and without."""
+    cases = []
+    for M, K, N in ((4096, 256, 264), (700, 1024, 512), (61, 512, 77)):
+        x, dy = inputs(M, M, M, K, N, dev, torch.bfloat16)
+        cases.append((*bgt.quantize_fp8(x), dy))
+    ref = [bgt.wgrad_fp8(*c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        got = []
+        for st in streams:
+            with torch.cuda.stream(st):
+                got.append([bgt.wgrad_fp8(*c) for c in cases])
+        torch.cuda.synchronize()
+        for out in got:
+            for a, b in zip(out, ref):
+                assert torch.equal(a, b)
 
 
 def test_gradient_of_the_product(bgt, dev):
@@ -123,6 +145,19 @@ def test_not_finite(bgt, dev, dtype):
     x[3, 130] = float("inf")
     dw = bgt.wgrad_fp8(*bgt.quantize_fp8(x), dy, 300)
     assert bool(dw[128:256].isnan().all()) and not bool(dw[:128].isnan().any()) and not bool(dw[256:].isnan().any())
+
+
+@pytest.mark.parametrize("N", [5, 50, 56])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_last_row_not_finite(bgt, dev, dtype, N):
+    """What fills up the last step of the rows takes nothing from the last row."""
+    x, dy = inputs(N, 67, 67, 256, N, dev, dtype)
+    dy[66, 1], dy[66, 3] = float("inf"), float("nan")
+    q, s = bgt.quantize_fp8(x)
+    dw = bgt.wgrad_fp8(q, s, dy)
+    assert plain.same(dw[:, 1].double(), plain.values(q, s)[66] * float("inf")) and bool(dw[:, 3].isnan().all())
+    rest = [n for n in range(N) if n not in (1, 3)]
+    check(dw[:, rest], plain.values(q, s), dy[:, rest])
 
 
 def test_many_elements(bgt, dev):
