@@ -6,7 +6,9 @@ with the router's k experts e and weights w of each token. Served with 4-bit exp
 weights: up to 64 tokens through the weight-only products of unquantized rows
 (w4a16_moe_gemv), more through the W4A8 integer-scale products (quantize_act,
 w4a8_moe_gemm_is). Trained with 16- or 32-bit experts: routing, gather and combine are
-autograd functions over the library's forward and backward calls.
+autograd functions over the library's forward and backward calls. Trained in 8-bit floating
+point: products of 8-bit rows and weights, activations kept in 8 bits for the backward pass, and
+the router's balance loss.
 
     python examples/moe_layer.py [--tokens 1 16 64 512] [--hidden 4096] [--inner 14336]
 """
@@ -113,6 +115,61 @@ def trained_layer(x, router, gate, up, down, k):
     return Combine.apply(torch.cat(ys), offs, pos, weights)
 
 
+class Fp8Experts(torch.autograd.Function):
+    """x -> the slots' rows (silu(x G_e) * (x U_e)) D_e with 8-bit products. Kept for the backward
+    pass: the rows, the gates and their product as 8-bit codes, and the turned weights."""
+
+    @staticmethod
+    def forward(ctx, x, offs, tok, pos, gate, up, down):
+        gate, up, down = (bgt.pack_weights_fp8(w.contiguous(), turned=True) for w in (gate, up, down))
+        qx, sx = bgt.quantize_fp8(x)
+        g, u = (bgt.w8a8_moe_gemm_fp8(qx, sx, offs, tok, w["qw"], w["sw"], out_dtype=x.dtype) for w in (gate, up))
+        kept = bgt.silu_mul_fp8(g, u)                # codes and scales of h, g and u
+        slots = torch.arange(g.shape[0], dtype=torch.int32, device=x.device)
+        ctx.save_for_backward(qx, sx, *kept, offs, tok, slots, pos, *(w[k] for w in (gate, up, down) for k in ("qt", "st")))
+        ctx.sizes = x.shape[1], g.shape[1]
+        return bgt.w8a8_moe_gemm_fp8(*kept[:2], offs, slots, down["qw"], down["sw"], out_dtype=x.dtype)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dys):
+        qx, sx, hq, hs, gq, gs, uq, us, offs, tok, slots, pos, *turned = ctx.saved_tensors
+        hidden, inner = ctx.sizes
+        dys = dys.contiguous()
+
+        def through(d, qt, st):
+            return bgt.w8a8_moe_gemm_fp8(*bgt.quantize_fp8(d), offs, slots, qt, st, out_dtype=d.dtype)
+
+        dg, du = bgt.silu_mul_fp8_backward(through(dys, *turned[4:]), gq, gs, uq, us)
+        dxs = through(dg, *turned[:2]) + through(du, *turned[2:4])
+        return (bgt.moe_gather_backward(dxs, pos), None, None, None, bgt.moe_wgrad_fp8(qx, sx, offs, tok, dg, hidden),
+                bgt.moe_wgrad_fp8(qx, sx, offs, tok, du, hidden), bgt.moe_wgrad_fp8(hq, hs, offs, slots, dys, inner))
+
+
+class Balance(torch.autograd.Function):
+    """The router's balance loss of logits and the experts that it chose."""
+
+    @staticmethod
+    def forward(ctx, logits, ids):
+        loss, counts, _, tokens = bgt.moe_balance(logits, ids)
+        ctx.save_for_backward(logits, counts, tokens)
+        return loss
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dloss):
+        return bgt.moe_balance_backward(dloss.contiguous(), *ctx.saved_tensors), None
+
+
+def fp8_layer(x, router, gate, up, down, k):
+    """The layer's output and the router's balance loss, for training; arguments as for
+    trained_layer."""
+    logits = x.float() @ router
+    weights, ids, offs, tok, pos = Route.apply(logits, k)
+    ys = Fp8Experts.apply(x, offs, tok, pos, gate, up, down)
+    return Combine.apply(ys, offs, pos, weights), Balance.apply(logits, ids)
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--tokens", type=int, nargs="*", default=[1, 16, 64, 512])
@@ -145,16 +202,25 @@ def main():
                                                         float(y.float().norm())), flush=True)
 
     h, i = 256, 512                                  # a small layer, a few steps
-    params = [torch.nn.Parameter(p) for p in (torch.randn(h, E, device=dev) / h ** 0.5,
-              *(0.05 * torch.randn(E, r, c, device=dev) for r, c in ((h, i), (h, i), (i, h))))]
-    opt = torch.optim.Adam(params, lr=3e-3)
     x, goal = torch.randn(1000, h, device=dev), torch.randn(1000, h, device=dev)
-    for step in range(5):
-        loss = (trained_layer(x, *params, a.topk) - goal).square().mean()
-        opt.zero_grad()
-        loss.backward()
-        opt.step()
-        print("train step %d: loss %.4f" % (step, float(loss.detach())), flush=True)
+
+    def full(*params):
+        return trained_layer(x, *params, a.topk), 0.0
+
+    def eight_bits(*params):
+        return fp8_layer(x, *params, a.topk)
+
+    for name, layer in (("train", full), ("train in 8 bits", eight_bits)):
+        params = [torch.nn.Parameter(p) for p in (torch.randn(h, E, device=dev) / h ** 0.5,
+                  *(0.05 * torch.randn(E, r, c, device=dev) for r, c in ((h, i), (h, i), (i, h))))]
+        opt = torch.optim.Adam(params, lr=3e-3)
+        for step in range(5):
+            y, balance = layer(*params)
+            loss = (y - goal).square().mean() + 0.01 * balance
+            opt.zero_grad()
+            loss.backward()
+            opt.step()
+            print("%s step %d: loss %.4f" % (name, step, float(loss.detach())), flush=True)
 
 
 if __name__ == "__main__":
