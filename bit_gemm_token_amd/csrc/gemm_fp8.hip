@@ -467,6 +467,9 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(2)
 #pragma unroll
     for (int i = 0; i < XCP; ++i) copy(xbase, xofs[i], g, S + BN * kGroup + (NW * i + wave) * 1024);
   };
+  // fp32: a wave whose rows all lie past the end only copies (a branch that 16-bit outputs' shorter
+  // steps lose more by: 1024 x 4096 into 4096 36 us, 28 without)
+  const bool idle = EX && m0 + wm * (BM / WM) >= M;
   const int64_t Ms = GR ? rt.T : M;
   int ssrc[FM];
 #pragma unroll
@@ -581,7 +584,7 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(2)
         scales(g + 1);
         issue(g + 1, nxt);
       }
-      compute(cur);
+      if (!idle) compute(cur);
       wait_lds0();
     };
 #pragma unroll 1
