@@ -15,6 +15,12 @@
 // (aligned bf16 rows); codes and the other types pass through registers, a step ahead, where
 // they are widened or split. Rows are XOR-swizzled by 64 bytes so that the four rows of a read
 // lie on distinct banks. Two LDS stages, one barrier a step.
+//
+// What bounds it: 32 rows of a 256 x 256 tile are 1024 cycles of matrix instructions for each term
+// of dy and, for bf16, as many of LDS traffic (96 KiB read, 32 KiB written), which have to overlap.
+// 8192 rows, 4096 x 4096: bf16 240 us (1145 TFLOP/s; a library product of bf16 operands 1361), fp16
+// 437 (629, 1258 in terms), fp32 668 (411, 1234 in terms; 644 in tiles of 256 x 256). Two columns of eight
+// rows a lane, paired by byte permutes, took 390, and of 4096 rows 345 and 469 (now 232 and 381).
 #include <algorithm>
 
 #include "fp8_common.h"
