@@ -651,7 +651,7 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(2)
     if (m0 + r >= M || n >= N) continue;
     uint16_t* o = yp + (int64_t)(r0 + m0 + r) * N + n;
     if (vec) {
-      *reinterpret_cast<uint4*>(o) = v;
+      store_once(o, v);
     } else {
       const uint16_t* h = reinterpret_cast<const uint16_t*>(&v);
 #pragma unroll

@@ -301,7 +301,7 @@ __global__ __launch_bounds__(SN * 2) __attribute__((amdgpu_waves_per_eu(2))) voi
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           const int k = k0 + wk * (SK / 2) + 32 * i + 8 * (r / 4) + 4 * hf + r % 4;
-          if (k < K) y[(int64_t)k * N + n] = acc[i][j][r];
+          if (k < K) __builtin_nontemporal_store(acc[i][j][r], y + (int64_t)k * N + n);
         }
     }
   } else if (sums) {
@@ -353,7 +353,7 @@ __global__ __launch_bounds__(SN * 2) __attribute__((amdgpu_waves_per_eu(2))) voi
         if (k >= K || n0 + 8 * (wn * 8 + c) >= N) continue;
         uint16_t* o = y + (int64_t)k * N + n;
         if (vec) {
-          *reinterpret_cast<uint4*>(o) = v;
+          store_once(o, v);
         } else {
           const uint16_t* e = reinterpret_cast<const uint16_t*>(&v);
 #pragma unroll
