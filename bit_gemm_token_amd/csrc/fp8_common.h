@@ -54,10 +54,14 @@ __device__ __forceinline__ void f8_unpack4(uint32_t w, float* v) {
   v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
 }
 
-// 16 bytes that this launch does not read again
+// stores past the L2, of outputs that nobody reads soon or that would push out what is shared
 __device__ __forceinline__ void store_once(void* p, uint4 v) {
   typedef uint32_t v4u __attribute__((ext_vector_type(4)));
   __builtin_nontemporal_store(__builtin_bit_cast(v4u, v), static_cast<v4u*>(p));
+}
+__device__ __forceinline__ void store_once(void* p, uint2 v) {
+  typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+  __builtin_nontemporal_store(__builtin_bit_cast(v2u, v), static_cast<v2u*>(p));
 }
 
 // eight consecutive elements of type IT at element i, widened: one or two 16-byte loads

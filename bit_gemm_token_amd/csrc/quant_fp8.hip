@@ -250,8 +250,9 @@ __global__ __launch_bounds__(kThreads) void k_f8_gate(
     if (m >= M) continue;
     const int64_t o = m * ((int64_t)G * kGroup) + c;
     *reinterpret_cast<uint2*>(hq + o) = codes_of(h, f8_scale(bh));
-    *reinterpret_cast<uint2*>(gq + o) = codes_of(g[s], f8_scale(bg));
-    *reinterpret_cast<uint2*>(uq + o) = codes_of(u[s], f8_scale(bu));
+    // g and u wait for the backward pass, h is read next (8192 x 14336 bf16 171 us without)
+    store_once(gq + o, codes_of(g[s], f8_scale(bg)));
+    store_once(uq + o, codes_of(u[s], f8_scale(bu)));
     if (threadIdx.x % kRowLanes == 0) {
       hs[(int64_t)b * M + m] = (uint8_t)bh;
       gs[(int64_t)b * M + m] = (uint8_t)bg;
