@@ -642,6 +642,11 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(2)
   __syncthreads();
   const bool vec = N % 8 == 0 && reinterpret_cast<uintptr_t>(y.p) % 16 == 0;
   uint16_t* yp = static_cast<uint16_t*>(y.p);
+  // 128 MB and more of outputs are stored past the L2 and leave the rows and weights there that tiles
+  // share (8192 x 4096 into 14336 437 us, 403 so); the next reader finds less in the caches, which
+  // costs it as much (quantizing those rows after: 500 and 498 together) or, of smaller outputs, more
+  // (4096^3: 60 and 61, together 70 and 74)
+  const bool past = (int64_t)(GR ? rt.R : M) * N >= 1 << 26;
 #pragma unroll 4
   for (int t = tid; t < BM * PIECES; t += NW * 64) {
     const int r = t / PIECES, piece = t % PIECES;
@@ -651,7 +656,8 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(2)
     if (m0 + r >= M || n >= N) continue;
     uint16_t* o = yp + (int64_t)(r0 + m0 + r) * N + n;
     if (vec) {
-      store_once(o, v);
+      if (past) store_once(o, v);
+      else *reinterpret_cast<uint4*>(o) = v;
     } else {
       const uint16_t* h = reinterpret_cast<const uint16_t*>(&v);
 #pragma unroll
