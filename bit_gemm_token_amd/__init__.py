@@ -1045,12 +1045,19 @@ def moe_balance(logits, ids, loss=None, counts=None, probs=None, tokens=None):
     k = ids.shape[1]
     need = lib().bgt_moe_balance_workspace_bytes(T, E)
     _raise("bgt_moe_balance_workspace_bytes", need if need < 0 else 0)
-    ws = torch.empty(need // 4, dtype=torch.int32, device=dev)
     loss = torch.empty((), dtype=torch.float32, device=dev) if loss is None else loss
     _check(loss, "loss", torch.float32, ())
-    counts = _out(counts, "counts", torch.int32, (E,), dev)
-    probs = _out(probs, "probs", torch.float32, (E,), dev)
-    tokens = _out(tokens, "tokens", torch.int32, (1,), dev)
+    if counts is None and probs is None and tokens is None and need <= 1 << 16:
+        # one allocation, whose parts cost the host less than three more (a loss of its own: callers
+        # change it in place)
+        ws, counts, tokens, probs = torch.empty(need // 4 + 2 * E + 1, dtype=torch.int32, device=dev) \
+            .split_with_sizes([need // 4, E, 1, E])
+        probs = probs.view(torch.float32)
+    else:
+        ws = torch.empty(need // 4, dtype=torch.int32, device=dev)
+        counts = _out(counts, "counts", torch.int32, (E,), dev)
+        probs = _out(probs, "probs", torch.float32, (E,), dev)
+        tokens = _out(tokens, "tokens", torch.int32, (1,), dev)
     _on(dev, ids=ids, loss=loss, counts=counts, probs=probs, tokens=tokens)
     _call("bgt_moe_balance", dev, _ptr(logits), lt, ld, _ptr(ids), T, E, k, _ptr(loss), _ptr(counts),
           _ptr(probs), _ptr(tokens), _ptr(ws), need)
