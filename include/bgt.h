@@ -544,10 +544,11 @@ int bgt_w4a16_moe_gemv(const void* x, int x_type, int64_t ldx, int64_t T,
  *              qt, K x N', st, (N'/128) x (K'/128), the same codes for the product over N
  *              (the gradient of x). Of E experts one after the other.
  * e is the least with max |x| <= 448 * 2^e, at least -117; codes are x / 2^e to nearest even,
- * so that a value is off by at most 2^-4 of itself or 2^-10 * 2^e, and a block of zeros is
- * exact. A block that holds an infinity or a NaN has the NaN exponent: all of its values are
- * NaN. Other codes and exponents than these calls write are accepted too; where products leave
- * fp32's normal range they may be flushed to zero.
+ * so that a value is off by at most 2^-4 of itself or 2^-10 * 2^e (from 1.9375 * 2^127 on it
+ * becomes 2^128, which fp32 and bf16 hold as an infinity), and a block of zeros is exact. A block
+ * that holds an infinity or a NaN has the NaN exponent: all of its values are NaN. Other codes
+ * and exponents than these calls write are accepted too; where products leave fp32's normal
+ * range they may be flushed to zero.
  * Common requirements: 1 <= M, T, R <= 2^24 rows, 1 <= K, N <= 2^18, 1 <= E <= 256; code
  * matrices 16-byte aligned, other pointers aligned to their elements (16-byte aligned rows that
  * are whole multiples of 16 bytes are faster). Sizes whose launch would pass 2^32 threads are
@@ -619,7 +620,8 @@ int bgt_moe_wgrad_fp8(const uint8_t* qx, const uint8_t* sx, int64_t T,
  * bgt_silu_mul_fp8 -- the gated activation of a feed-forward layer, h = silu(g) * u with
  * silu(g) = g / (1 + exp(-g)), computed in fp32 and stored as rows in 8 bits (the next
  * product's operand), together with g and u in 8 bits, which is all that the backward call
- * needs. gate, up: M x K of `type`, row strides ldg, ldu >= K (two halves of one matrix, say).
+ * needs. For g below -87, where 1 / (1 + exp(-g)) leaves fp32's normal range, h may be 0.
+ * gate, up: M x K of `type`, row strides ldg, ldu >= K (two halves of one matrix, say).
  */
 int bgt_silu_mul_fp8(const void* gate, int64_t ldg, const void* up, int64_t ldu, int type,
                      int64_t M, int64_t K, uint8_t* hq, uint8_t* hs, uint8_t* gq, uint8_t* gs,

@@ -215,3 +215,32 @@ def test_many_elements(bgt, dev):
     assert not bool(q[:-40].view(torch.uint8).any())
     y = bgt.dequantize_fp8(q, s, out_dtype=torch.bfloat16)
     assert torch.equal(y[-40:], (codes.view(40, -1, 128) * torch.exp2(e.t())[..., None]).view(40, -1).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_gate_not_finite(bgt, dev, dtype, which, bad):
+    """What is not finite in gate or up makes its block of that and of the product NaN, no other."""
+    rows = gate_rows(12, 9, 300, dev, dtype)[:2]
+    clean = bgt.silu_mul_fp8(*rows)
+    rows[which][4, 140] = bad
+    out = bgt.silu_mul_fp8(*rows)
+    for i in range(3):                                        # h, gate, up
+        v, c = bgt.dequantize_fp8(*out[2 * i:2 * i + 2]), bgt.dequantize_fp8(*clean[2 * i:2 * i + 2])
+        if i in (0, 1 + which):
+            assert bool(v[4, 128:256].isnan().all())
+            v[4, 128:256] = c[4, 128:256]
+        assert torch.equal(v, c)
+
+
+def test_gate_at_the_ends_of_fp32(bgt, dev):
+    """Gates up to the largest fp32 value, and products that pass it."""
+    top = torch.finfo(torch.float32).max
+    g = torch.tensor([-top, top, -3e38, 2.5e38, -87.0, 87.0, -104.0, 104.0], device=dev).repeat(16)[None]
+    h = plain.values(*bgt.silu_mul_fp8(g, torch.ones_like(g))[:2])   # top rounds to 2^128, past fp32
+    ref = torch.nn.functional.silu(g.double())
+    # codes of 2^-4, on a block whose largest is top: below 2^-9 of 2^e = top / 448 they are 0
+    assert bool(((h - ref).abs() <= 2.0 ** -4 * ref.abs() + 2.0 ** -10 * 2.0 ** 120).all())
+    over = bgt.dequantize_fp8(*bgt.silu_mul_fp8(g, torch.full_like(g, 4.0))[:2])
+    assert bool(over.isnan().all())                           # an infinity in the block
