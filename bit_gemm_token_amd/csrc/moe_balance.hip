@@ -4,7 +4,7 @@
 //     loss = E sum_e f_e P_e,   P_e = (1 / T') sum_t p_te
 //     dl_te = dloss (E / T') p_te (f_e - sum_j f_j p_tj)       (f is a constant of the gradient)
 //
-// T': the tokens with a logit above -inf; the others (padding) have p_t = 0 and no gradient.
+// T': the tokens with a logit other than -inf; the others (padding) have p_t = 0 and no gradient.
 //
 // A token's logits lie in L = 1 .. 64 lanes, four each, so that its softmax takes lane exchanges
 // only; a lane adds up its own four experts' probabilities over its tokens in registers, the
@@ -44,7 +44,9 @@ __device__ __forceinline__ float group_sum(float v) {
   for (int o = 1; o < L; o <<= 1) v += __shfl_xor(v, o, kWave);
   return v;
 }
-// the softmax of a token's logits over its L lanes; false where none is above -inf (p = 0)
+// the softmax of a token's logits over its L lanes; false where all are -inf (p = 0). The maximum
+// passes over NaN, the sum does not: it is 0 only if every term is, so that a token of NaN and
+// -inf alone is NaN too, as the formula is.
 template <int L, int IT>
 __device__ __forceinline__ bool softmax4(const void* logits, int64_t row, int e0, int E, float* p) {
   float v[kEach], top = -INFINITY;
@@ -54,7 +56,7 @@ __device__ __forceinline__ bool softmax4(const void* logits, int64_t row, int e0
     top = fmaxf(top, v[j]);
   }
   top = group_max<L>(top);
-  const bool some = top > -INFINITY;                
+  if (top == -INFINITY) top = 0.0f;
   float sum = 0.0f;
 #pragma unroll
   for (int j = 0; j < kEach; ++j) {
@@ -62,6 +64,7 @@ __device__ __forceinline__ bool softmax4(const void* logits, int64_t row, int e0
     sum += p[j];
   }
   sum = group_sum<L>(sum);
+  const bool some = !(sum == 0.0f);
 #pragma unroll
   for (int j = 0; j < kEach; ++j) p[j] = some ? p[j] / sum : 0.0f;
   return some;

@@ -638,7 +638,7 @@ int bgt_silu_mul_fp8_backward(const void* dh, int type, int64_t ld, const uint8_
  * bgt_moe_balance -- balance loss of a router, with the experts' counts: with p_t the softmax
  * of token t's logits over all E experts, c_e the number of ids equal to e, f_e = c_e / sum c,
  *     P_e = (1/T') sum_t p_te,   loss = E sum_e f_e P_e   (1 where both are even),
- * T' the tokens that have a logit above -inf; the others (padding) have p_t = 0. ids outside
+ * T' the tokens that have a logit other than -inf; the others (padding) have p_t = 0. ids outside
  * [0, E) are no expert's. 0 where no token or no id is left. fp32 sums of at most a workgroup's
  * tokens, added up in fp64. NaN logits and logits of +inf make p_t NaN as the formula does.
  *   logits  T x E of `type`, row stride ld >= E;  ids  T x k int32 (as bgt_moe_route leaves them)
@@ -653,8 +653,8 @@ int64_t bgt_moe_balance_workspace_bytes(int64_t T, int64_t E);
 
 /* bgt_moe_balance_backward -- gradient of the logits from that of the loss (one float32 on the
  * device), counts being constants:
- *     dl_te = dloss (E/T') p_te (f_e - sum_j f_j p_tj),   zeros for tokens without a logit
- * above -inf. counts and tokens: the forward call's, or their sums over the ranks of a job.
+ *     dl_te = dloss (E/T') p_te (f_e - sum_j f_j p_tj),   zeros for tokens whose logits
+ * are all -inf. counts and tokens: the forward call's, or their sums over the ranks of a job.
  * dlogits: T x E of `type`, dense. */
 int bgt_moe_balance_backward(const float* dloss, const void* logits, int type, int64_t ld,
                              const int32_t* counts, const int32_t* tokens, int64_t T, int64_t E,

@@ -1,0 +1,47 @@
+"""A router's balance loss and its gradient at their edges."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+TYPES = [torch.float32, torch.float16, torch.bfloat16]
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return torch.device("cuda:0")
+
+
+@pytest.fixture(scope="module")
+def bgt():
+    import bit_gemm_token_amd
+    bit_gemm_token_amd.lib()
+    return bit_gemm_token_amd
+
+
+# one workgroup and many; one, two, sixteen and all lanes of a wave for a token
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("others", [NAN, -INF])
+@pytest.mark.parametrize("T,E", [(5, 3), (40, 8), (3000, 60), (2000, 256)])
+def test_token_of_nan(bgt, dev, T, E, others, dtype):
+    """A token whose logits are NaN, all of them or one among -inf, is no padding: it counts, and makes
+    the loss, P and its own gradient NaN."""
+    g = torch.Generator(device=dev).manual_seed(T)
+    logits = torch.randn(T, E, generator=g, device=dev).to(dtype)
+    ids = torch.randint(0, E, (T, 2), generator=g, device=dev, dtype=torch.int32)
+    logits[1] = -INF                                            # padding
+    clean = bgt.moe_balance(logits, ids)
+    bad = T // 2
+    logits[bad] = others
+    logits[bad, E - 1] = NAN
+    loss, counts, probs, tokens = bgt.moe_balance(logits, ids)
+    assert int(tokens) == T - 1 == int(clean[3]) and torch.equal(counts, clean[1])
+    assert bool(loss.isnan()) and bool(probs.isnan().all())
+    d = bgt.moe_balance_backward(torch.ones((), device=dev), logits, counts, tokens)
+    assert bool(d[bad].isnan().all()) and not bool(d[1].any())
+    d[bad] = 0
+    assert not bool(d.isnan().any()) and bool(d.any())
