@@ -14,6 +14,7 @@ namespace bgt {
 
 constexpr uint32_t kF8MinByte = 10;                  // 2^-117
 constexpr uint32_t kF8NanByte = 255;
+constexpr float kF8Nan = __builtin_nanf("");
 
 // exponent byte of a block from the largest |x| as float bits (integer order: an infinity
 // or a NaN in the block wins, and gives the NaN byte). 448 = 1.75 * 2^8: a mantissa above

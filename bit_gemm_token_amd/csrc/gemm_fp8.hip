@@ -10,7 +10,8 @@
 // error of about 1.4e-5 of the sum for normal data at K = 128: far below the rounding of a
 // 16-bit output, but not of an fp32 one. Outputs in fp32 therefore take bf16 products of the
 // same codes (e4m3 is exact in bf16, the products exact in fp32, four instructions in place of
-// one), with the group's scale applied to its fp32 sum.
+// one), with the sum of the two exponents applied to its fp32 sum at once: one alone may take the
+// sum out of range (rows of 2^118 by weights of 2^-20).
 //
 // The order of k within a group is free as long as both operands agree: a lane takes 16-byte
 // pieces where they are contiguous for its neighbours.
@@ -319,6 +320,7 @@ __global__ __launch_bounds__(stream_waves(MT, CH) * 64) void k_f8_stream(
     v4f acc[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    uint32_t worst[MT] = {};                          // of the exponent bytes: 255 makes the sum NaN
 #pragma unroll 1
     for (int ch = 0; ch < chunks; ++ch) {
       if constexpr (CH) {
@@ -335,9 +337,10 @@ __global__ __launch_bounds__(stream_waves(MT, CH) * 64) void k_f8_stream(
 #pragma unroll
             for (int u = 0; u < 4; ++u)
               p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(w, u), widen8(xc[j][m], u), p, 0, 0, 0);
-            const float a = f8_scale(sxb[j][m]), b = f8_scale(sb[j]);
+            const int e = (int)(sxb[j][m] + sb[j]) - 254;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[m][r] = acc[m][r] + p[r] * a * b;
+            for (int r = 0; r < 4; ++r) acc[m][r] = acc[m][r] + __builtin_ldexpf(p[r], e);
+            worst[m] = umax(worst[m], umax(sxb[j][m], sb[j]));
           } else {
             acc[m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, xc[j][m], acc[m], 0, 0, 0,
                                                                       (int)sb[j], 0, (int)sxb[j][m]);
@@ -350,9 +353,11 @@ __global__ __launch_bounds__(stream_waves(MT, CH) * 64) void k_f8_stream(
     }
     // lane: row m = 16 mt + lane % 16, outputs n = 4 (lane / 16) + r
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < MT; ++m) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) red[buf][(wave * MT * 4 + m * 4 + r) * 64 + lane] = acc[m][r];
+      for (int r = 0; r < 4; ++r)
+        red[buf][(wave * MT * 4 + m * 4 + r) * 64 + lane] = EX && worst[m] == kF8NanByte ? kF8Nan : acc[m][r];
+    }
     __syncthreads();
     if (single) {
       if ((int)threadIdx.x < MT * 256) sum(threadIdx.x, late, value);
@@ -395,9 +400,10 @@ template <class T, class F> struct Pick<false, T, F> { using type = F; };
 // (two sets of registers), so that a group's two LDS reads and its copies run under the products;
 // its copies are 32-bit offsets from one base in scalar registers, for want of vector registers
 // (8192 x 14336 into 4096: 391 us, 425 without; 8192^3 467 and 474). Smaller tiles lose by it
-// (128 x 128, 8192^3: 576 and 532): more workgroups a CU do the same for them.
+// (128 x 128, 8192^3: 576 and 532): more workgroups a CU do the same for them. fp32: eight waves of
+// at most 128 registers, so that two workgroups share a CU.
 template <int BN, int BM, int WN, int WM, bool EX, bool GR>
-__global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(2))) void k_f8_tile(
+__global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(EX ? 4 : 2))) void k_f8_tile(
     const uint8_t* __restrict__ qx, const uint8_t* __restrict__ sx, const uint8_t* __restrict__ qw,
     const uint8_t* __restrict__ sw, int M, int N, int K, OutY y, Route rt) {
   constexpr int NW = WN * WM;
@@ -506,6 +512,7 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(2)
 #pragma unroll
     for (int m = 0; m < FM; ++m) xx[m] = fragment(S + BN * kGroup, wm * (BM / WM) + 32 * m + lr, h);
   };
+  uint32_t worst[FM] = {};                             // fp32: of the exponent bytes, 255 makes the sum NaN
   auto multiply = [&](const v8i* w, const v8i* xx) {
 #pragma unroll
     for (int i = 0; i < FN; ++i)
@@ -563,9 +570,10 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(2)
               for (int u = 0; u < 4; ++u)
                 p = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen8(w, u), widen8(xx, u), p, 0, 0, 0);
             }
-            const float a = f8_scale(sa[m]), b = f8_scale(sb);
+            const int e = (int)(sa[m] + sb) - 254;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][m][r] = acc[i][m][r] + p[r] * a * b;
+            for (int r = 0; r < 16; ++r) acc[i][m][r] = acc[i][m][r] + __builtin_ldexpf(p[r], e);
+            worst[m] = umax(worst[m], umax(sa[m], sb));
           }
       } else {
 #pragma unroll
@@ -602,6 +610,7 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(2)
       for (int m = 0; m < FM; ++m) {
         const int row = m0 + wm * (BM / WM) + 32 * m + lr;
         if (row >= M) continue;
+        if (worst[m] == kF8NanByte) acc[i][m] = v16f{} + kF8Nan;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int n = n0 + wn * (BN / WN) + 32 * i + 8 * q + 4 * hf;

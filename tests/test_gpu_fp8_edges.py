@@ -1,0 +1,74 @@
+"""8-bit floating-point operators at the edges of their types' ranges, against 64 bits."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+import fp8_plain as plain  # noqa: E402
+
+TYPES = [torch.float32, torch.float16, torch.bfloat16]
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return torch.device("cuda:0")
+
+
+@pytest.fixture(scope="module")
+def bgt():
+    import bit_gemm_token_amd
+    bit_gemm_token_amd.lib()
+    return bit_gemm_token_amd
+
+
+def within(y, x, w, dtype):
+    ref = x @ w
+    bound = plain.product_bound(x, w, ref, dtype)
+    assert bool(y.isfinite().all())
+    assert bool(((y.double() - ref).abs() <= bound).all()), float(((y.double() - ref).abs() / bound).max())
+
+
+# powers of two of x and w whose product is well within the types; fp16 holds sums of 256 products of
+# 2^6 (at most 3.61 * 2^14 = 59146), and no more of them
+FAR = [(118, -20), (-20, 118), (118, -112), (-112, 118), (127, -122), (-122, 127)]
+
+
+@pytest.mark.parametrize("a,b", FAR)
+@pytest.mark.parametrize("M,K", [(1, 128), (1, 256), (20, 256), (60, 256), (300, 256), (1, 4224), (20, 4224), (60, 4224)])
+def test_products_of_far_scales(bgt, dev, M, K, a, b):
+    """Neither factor's scale alone takes a sum out of range, whichever is the large one; groups of
+    either sign."""
+    N = 40
+    g = torch.Generator(device=dev).manual_seed(M + K)
+    x = (1 + 0.9 * torch.rand(M, K, generator=g, device=dev)) * 2.0 ** a
+    w = (1 + 0.9 * torch.rand(K, N, generator=g, device=dev)) * 2.0 ** b
+    x[:, 128:256] *= -0.5
+    q, s = bgt.quantize_fp8(x)
+    p = bgt.pack_weights_fp8(w)
+    for dtype in TYPES if a + b <= 6 and K <= 256 else TYPES[::2]:
+        y = bgt.w8a8_gemm_fp8(q, s, p["qw"], p["sw"], out_dtype=dtype)
+        within(y, plain.values(q, s), plain.matrix(p["qw"], p["sw"]), dtype)
+        z = bgt.w8a8_linear_fp8(x, p["qw"], p["sw"], out_dtype=dtype)[0]
+        within(z, plain.values(q, s), plain.matrix(p["qw"], p["sw"]), dtype)
+
+
+@pytest.mark.parametrize("a,b", FAR)
+@pytest.mark.parametrize("T,K", [(3, 256), (30, 256), (90, 256), (400, 256), (30, 4224)])
+def test_routed_products_of_far_scales(bgt, dev, T, K, a, b):
+    E, N = 2, 40
+    g = torch.Generator(device=dev).manual_seed(T + K)
+    x = (1 + 0.9 * torch.rand(T, K, generator=g, device=dev)) * 2.0 ** a
+    w = (1 + 0.9 * torch.rand(E, K, N, generator=g, device=dev)) * 2.0 ** b
+    x[:, 128:256] *= -0.5
+    offs, tok, expert = plain.route(plain.ids_of(g, T, E, 1, 0.1, dev), E)
+    q, s = bgt.quantize_fp8(x)
+    p = bgt.pack_weights_fp8(w)
+    for dtype in TYPES if a + b <= 6 and K <= 256 else TYPES[::2]:
+        y = bgt.w8a8_moe_gemm_fp8(q, s, offs, tok, p["qw"], p["sw"], out_dtype=dtype)
+        v = plain.values(q, s)
+        for e in range(E):
+            i, j = int(offs[e]), int(offs[e + 1])
+            if i < j:
+                within(y[i:j], v[tok[i:j].long()], plain.matrix(p["qw"][e], p["sw"][e]), dtype)
