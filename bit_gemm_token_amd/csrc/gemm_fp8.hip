@@ -680,11 +680,12 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(EX
 namespace {
 
 // waves: as many as the groups; workgroups: enough for 16 waves a CU (8 for 64 rows: registers),
-// no more than items (of a route: than its slots may need)
+// no more than items (of a route: than its slots may need). Without `run`, here and below: only whether
+// the launch is within the grid's limits.
 template <int MT, int GPW, bool CH, bool EX, int XT, bool GR>
 hipError_t stream_t(const void* x, int64_t ldx, int64_t Kx, const uint8_t* sx, const uint8_t* qw,
                     const uint8_t* sw, int64_t M, int64_t N, int64_t K, OutY y, const Route& rt,
-                    uint8_t* q_out, uint8_t* s_out, hipStream_t stream) {
+                    uint8_t* q_out, uint8_t* s_out, hipStream_t stream, bool run = true) {
   const int64_t G = K / kGroup;
   int waves = 1;
   while (waves < stream_waves(MT, CH) && waves < G) waves *= 2;
@@ -692,6 +693,7 @@ hipError_t stream_t(const void* x, int64_t ldx, int64_t Kx, const uint8_t* sx, c
   const int64_t items = blocks * ((N + 15) / 16);
   const int64_t wgs = std::min<int64_t>(items, device_cus() * ((MT == 4 ? 8 : 16) / waves)) + (GR ? kZeroWgs : 0);
   if (items > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  if (!run) return hipSuccess;
   hipLaunchKernelGGL((k_f8_stream<MT, GPW, CH, EX, XT, GR>), dim3((unsigned)wgs), dim3(waves * kWave), 0,
                      stream, x, ldx, (int)Kx, sx, qw, sw, (int)M, (int)N, (int)K, y, rt, q_out, s_out);
   return hipGetLastError();
@@ -704,12 +706,12 @@ constexpr int kStreamRows = 64;                       // rows of a matrix that t
 template <bool EX, bool GR>
 hipError_t stream_rows(const uint8_t* qx, const uint8_t* sx, const uint8_t* qw, const uint8_t* sw,
                        int64_t M, int64_t N, int64_t K, OutY y, const Route& rt, int64_t per,
-                       hipStream_t stream) {
+                       hipStream_t stream, bool run) {
   const bool all = K <= kStreamGroups * kGroup;       // 16 waves of 2 groups, 8 of 4
   // experts' slots scatter about their mean, and one past the block reads its weights again
   if (GR) per += per / 2;
 #define BGT_STREAM(MT, GPW, CH) \
-  return stream_t<MT, GPW, CH, EX, -1, GR>(qx, K, K, sx, qw, sw, M, N, K, y, rt, nullptr, nullptr, stream)
+  return stream_t<MT, GPW, CH, EX, -1, GR>(qx, K, K, sx, qw, sw, M, N, K, y, rt, nullptr, nullptr, stream, run)
   if (per <= 16) {
     if (all) BGT_STREAM(1, 2, false);
     BGT_STREAM(1, 2, true);
@@ -725,11 +727,12 @@ hipError_t stream_rows(const uint8_t* qx, const uint8_t* sx, const uint8_t* qw, 
 
 template <int BN, int BM, int WN, int WM, bool EX, bool GR>
 hipError_t tile_t(const uint8_t* qx, const uint8_t* sx, const uint8_t* qw, const uint8_t* sw, int64_t M,
-            int64_t N, int64_t K, OutY y, const Route& rt, hipStream_t stream) {
+            int64_t N, int64_t K, OutY y, const Route& rt, hipStream_t stream, bool run) {
   const int64_t ntn = (N + BN - 1) / BN;
   const int64_t wgs = GR ? (rt.R / BM + std::min<int64_t>(rt.E, rt.R)) * ntn + kZeroWgs
                          : (M + BM - 1) / BM * ntn;
   if (!grid_fits(wgs, WN * WM * 64)) return hipErrorInvalidConfiguration;
+  if (!run) return hipSuccess;
   hipLaunchKernelGGL((k_f8_tile<BN, BM, WN, WM, EX, GR>), dim3((unsigned)wgs), dim3(WN * WM * 64), 0,
                      stream, qx, sx, qw, sw, (int)M, (int)N, (int)K, y, rt);
   return hipGetLastError();
@@ -737,13 +740,14 @@ hipError_t tile_t(const uint8_t* qx, const uint8_t* sx, const uint8_t* qw, const
 
 template <bool GR>
 hipError_t launch_t(const uint8_t* qx, const uint8_t* sx, const uint8_t* qw, const uint8_t* sw,
-                    int64_t M, int64_t N, int64_t K, OutY y, const Route& rt, hipStream_t stream) {
+                    int64_t M, int64_t N, int64_t K, OutY y, const Route& rt, hipStream_t stream,
+                    bool run = true) {
   const bool ex = y.type == kF32;
   const int64_t per = GR ? (rt.R + rt.E - 1) / rt.E : M;      // rows of a matrix
   if (per <= kStreamRows)
-    return ex ? stream_rows<true, GR>(qx, sx, qw, sw, M, N, K, y, rt, per, stream)
-              : stream_rows<false, GR>(qx, sx, qw, sw, M, N, K, y, rt, per, stream);
-  if (ex) return tile_t<128, 128, 2, 4, true, GR>(qx, sx, qw, sw, M, N, K, y, rt, stream);
+    return ex ? stream_rows<true, GR>(qx, sx, qw, sw, M, N, K, y, rt, per, stream, run)
+              : stream_rows<false, GR>(qx, sx, qw, sw, M, N, K, y, rt, per, stream, run);
+  if (ex) return tile_t<128, 128, 2, 4, true, GR>(qx, sx, qw, sw, M, N, K, y, rt, stream, run);
   // The largest tile that keeps the CUs busy, one workgroup each of 256 x 256, two and more of the
   // smaller ones (us): 8192 x 14336 into 4096, 512 tiles of 256 x 256: 393, of 128 x 128 459;
   // 1024 x 4096 into 14336, 224 tiles: 62.6 and 71.6; 2048 x 4096 into 4096, 128 tiles: 55.3, 38.1;
@@ -756,10 +760,10 @@ hipError_t launch_t(const uint8_t* qx, const uint8_t* sx, const uint8_t* qw, con
   const int64_t busy = (int64_t)device_cus() * 4 / 5;
   const bool near = !GR || (int64_t)rt.T * K < (1LL << 32);    // rows of x within 32-bit offsets
   if (tiles(256) >= busy && per >= 256 && near)
-    return tile_t<256, 256, 4, 2, false, GR>(qx, sx, qw, sw, M, N, K, y, rt, stream);
+    return tile_t<256, 256, 4, 2, false, GR>(qx, sx, qw, sw, M, N, K, y, rt, stream, run);
   if (tiles(128) >= busy)
-    return tile_t<128, 128, 2, 2, false, GR>(qx, sx, qw, sw, M, N, K, y, rt, stream);
-  return tile_t<64, 64, 2, 2, false, GR>(qx, sx, qw, sw, M, N, K, y, rt, stream);
+    return tile_t<128, 128, 2, 2, false, GR>(qx, sx, qw, sw, M, N, K, y, rt, stream, run);
+  return tile_t<64, 64, 2, 2, false, GR>(qx, sx, qw, sw, M, N, K, y, rt, stream, run);
 }
 
 }  // namespace
@@ -783,11 +787,12 @@ hipError_t launch_w8a8_f8_linear(const void* x, int type, int64_t ldx, int64_t K
   // more for the codes about 10), not for longer K, where every item would do it again
   const bool fused = M <= kFusedRows && K <= kStreamGroups * kGroup && Kx % 8 == 0 &&
                      reinterpret_cast<uintptr_t>(x) % 16 == 0 && ldx * (type == kF32 ? 4 : 2) % 16 == 0;
-  if (!fused) {
-    const hipError_t e = launch_f8_rows(x, type, M, Kx, ldx, q, s, stream);
+  const Route rt{};
+  if (!fused) {                                       // the product's limits before the rows' launch
+    hipError_t e = launch_t<false>(q, s, qw, sw, M, N, K, y, rt, stream, false);
+    if (e == hipSuccess) e = launch_f8_rows(x, type, M, Kx, ldx, q, s, stream);
     return e != hipSuccess ? e : launch_w8a8_f8(q, s, qw, sw, M, N, K, y, stream);
   }
-  const Route rt{};
   const bool ex = y.type == kF32;
 #define BGT_FUSED(T)                                                                                      \
   return ex ? stream_t<1, 2, false, true, T, false>(x, ldx, Kx, nullptr, qw, sw, M, N, K, y, rt, q, s, stream) \
