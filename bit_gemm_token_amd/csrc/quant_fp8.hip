@@ -295,8 +295,11 @@ __global__ __launch_bounds__(kThreads) void k_f8_gate_grad(
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float gj = g[j] * sg[s], uj = u[j] * su[s], sig = sigmoid(gj);
-      a[j] = d[s][j] * uj * sig * (1.0f + gj * (1.0f - sig));
-      d[s][j] = d[s][j] * gj * sig;
+      // the larger of dh and u meets the small factor first: dh u alone may leave fp32's range
+      const float f = sig * (1.0f + gj * (1.0f - sig)), dj = d[s][j];
+      const bool up = fabsf(uj) > fabsf(dj);
+      a[j] = (up ? uj : dj) * f * (up ? dj : uj);
+      d[s][j] = dj * (gj * sig);
     }
     if constexpr (VEC) {
       if (c < K) {

@@ -72,3 +72,24 @@ def test_routed_products_of_far_scales(bgt, dev, T, K, a, b):
             i, j = int(offs[e]), int(offs[e + 1])
             if i < j:
                 within(y[i:j], v[tok[i:j].long()], plain.matrix(p["qw"][e], p["sw"][e]), dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES[::2])
+@pytest.mark.parametrize("K", [128, 130])
+@pytest.mark.parametrize("g,u,dh", [(-24, 2.0 ** 60, 2.0 ** 80), (-60, 2.0 ** 30, 2.0 ** 120), (-80, 2.0 ** 100, 2.0 ** 120),
+                                    (-80, 2.0 ** 120, 2.0 ** 100), (-60, 2.0 ** -80, 2.0 ** 126), (-60, 2.0 ** 126, 2.0 ** -80)])
+def test_gate_gradient_in_range(bgt, dev, dtype, K, g, u, dh):
+    """Gradients that are finite though dh u or dh g is not, and not lost where one factor is small."""
+    rnd = torch.Generator(device=dev).manual_seed(K)
+    up = u * (1 + torch.rand(5, K, generator=rnd, device=dev))
+    gate = torch.full_like(up, g)
+    d = (dh * (1 + torch.rand(5, K, generator=rnd, device=dev))).to(dtype)
+    kept = (*bgt.quantize_fp8(gate), *bgt.quantize_fp8(up))
+    got = bgt.silu_mul_fp8_backward(d, *kept)
+    gv, uv, dd = plain.values(*kept[:2])[:, :K], plain.values(*kept[2:])[:, :K], d.double()
+    s = torch.sigmoid(gv)
+    for y, ref in zip(got, (dd * uv * s * (1 + gv * (1 - s)), dd * gv * s)):
+        assert bool((ref.abs() < torch.finfo(dtype).max).all())
+        # at most 32 roundings to fp32: the sigmoid's dozen, the factors and their products. dh of 2^-80
+        # times silu(-60) of about 2^-81 lies below the normal range, where a result may be 0.
+        assert bool(((y.double() - ref).abs() <= (32 * 2.0 ** -24 + torch.finfo(dtype).eps / 2) * ref.abs() + torch.finfo(dtype).tiny).all())
