@@ -404,7 +404,8 @@ Plan wgrad_plan(int type, int64_t M, int64_t K, int64_t N, int64_t E) {
 template <int SK, int SN, int ROWS, int DT, int LOAD, bool GR>
 hipError_t wgrad_t(const Plan& p, const uint8_t* qx, const uint8_t* sx, const void* dy, int64_t ld, int64_t M,
                    int64_t K, int64_t N, const Route& rt, OutY dw, float* ws, hipStream_t stream) {
-  if (!grid_fits(p.tiles, SN * 2) || !grid_fits((K * N + 255) / 256, 256)) return hipErrorInvalidConfiguration;
+  if (!grid_fits(p.tiles, SN * 2) || (p.parts > 1 && !grid_fits((K * N + 255) / 256, 256)))
+    return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL((k_f8_wgrad<SK, SN, ROWS, DT, LOAD, GR>),
                      dim3((unsigned)p.tiles, (unsigned)(GR ? rt.E : p.parts)), dim3(SN * 2), 0, stream, qx, sx,
                      dy, ld, (int)M, (int)K, (int)N, rt, dw, p.parts, ws);

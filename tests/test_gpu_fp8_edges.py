@@ -93,3 +93,18 @@ def test_gate_gradient_in_range(bgt, dev, dtype, K, g, u, dh):
         # at most 32 roundings to fp32: the sigmoid's dozen, the factors and their products. dh of 2^-80
         # times silu(-60) of about 2^-81 lies below the normal range, where a result may be 0.
         assert bool(((y.double() - ref).abs() <= (32 * 2.0 ** -24 + torch.finfo(dtype).eps / 2) * ref.abs() + torch.finfo(dtype).tiny).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES[::2])
+def test_weight_gradient_of_2_32_elements(bgt, dev, dtype):
+    """As many outputs as a grid's threads, where no parts are joined: a wide vocabulary's gradient."""
+    M, K, N = 4, 1 << 16, 1 << 16
+    g = torch.Generator(device=dev).manual_seed(1)
+    q, s = bgt.quantize_fp8(torch.randn(M, K, generator=g, device=dev))
+    dy = torch.randn(M, N, generator=g, device=dev).to(dtype)
+    dw = bgt.wgrad_fp8(q, s, dy)
+    assert dw.shape == (K, N)
+    x = plain.values(q, s)
+    for k in (0, 1, 127, 12345, 32768, 65407, 65535):
+        ref, size = x[:, k] @ dy.double(), x[:, k].abs() @ dy.double().abs()
+        assert bool(((dw[k].double() - ref).abs() <= M * 2.0 ** -23 * size + torch.finfo(dtype).eps / 2 * ref.abs()).all())
