@@ -223,18 +223,15 @@ __global__ __launch_bounds__(kBThreads) void k_balance_grad(
     const float* __restrict__ dloss, const void* __restrict__ logits, int64_t ld,
     const int32_t* __restrict__ counts, const int32_t* __restrict__ tokens, int T, int E, OutY d) {
   const int tid = threadIdx.x, e0 = tid % L * kEach;
-  int n = 0;
-  float f[kEach];
+  float n = 0.0f, f[kEach];                           // n: exact up to 2^24, the counts of one call
 #pragma unroll
   for (int j = 0; j < kEach; ++j) {
-    const int c = e0 + j < E ? counts[e0 + j] : 0;
-    f[j] = (float)c;
-    n += c;
+    f[j] = e0 + j < E ? (float)counts[e0 + j] : 0.0f;
+    n += f[j];
   }
+  n = group_sum<L>(n);                                // sums over many ranks may pass 2^31
 #pragma unroll
-  for (int o = 1; o < L; o <<= 1) n += __shfl_xor(n, o, kWave);
-#pragma unroll
-  for (int j = 0; j < kEach; ++j) f[j] = n > 0 ? f[j] / (float)n : 0.0f;
+  for (int j = 0; j < kEach; ++j) f[j] = n > 0.0f ? f[j] / n : 0.0f;
   const int valid = *tokens;
   const float scale = valid > 0 ? *dloss * (float)E / (float)valid : 0.0f;
   for (int64_t t = (int64_t)blockIdx.x * (kBThreads / L) + tid / L; t < T;

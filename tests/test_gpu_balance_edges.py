@@ -45,3 +45,22 @@ def test_token_of_nan(bgt, dev, T, E, others, dtype):
     assert bool(d[bad].isnan().all()) and not bool(d[1].any())
     d[bad] = 0
     assert not bool(d.isnan().any()) and bool(d.any())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("E", [2, 8, 100])
+def test_counts_of_many_ranks(bgt, dev, E, dtype):
+    """Counts whose sum passes 2^31, as the sums over a job's ranks may."""
+    g = torch.Generator(device=dev).manual_seed(E)
+    logits = torch.randn(50, E, generator=g, device=dev).to(dtype)
+    counts = torch.randint(1 << 29, (1 << 31) - 1, (E,), generator=g, device=dev, dtype=torch.int64).to(torch.int32)
+    counts[0] = (1 << 31) - 1
+    counts[-1] = 1 << 30
+    tokens = torch.tensor([1 << 30], dtype=torch.int32, device=dev)
+    got = bgt.moe_balance_backward(torch.tensor(2.0 ** 30, device=dev), logits, counts, tokens)
+    p, f = torch.softmax(logits.double(), 1), counts.double() / float(counts.double().sum())
+    dot = (p * f).sum(1, keepdim=True)
+    ref = E * p * (f - dot)
+    # softmax of E terms, the counts' sum and the dot product: at most 100 + E / 4 roundings to fp32
+    bound = (100 + E / 4) * 2.0 ** -24 * E * p * (f + dot) + torch.finfo(dtype).eps / 2 * ref.abs() * 1.01 + torch.finfo(dtype).tiny
+    assert bool(((got.double() - ref).abs() <= bound).all()) and bool(got.any())
