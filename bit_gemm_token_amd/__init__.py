@@ -1048,11 +1048,11 @@ def moe_balance(logits, ids, loss=None, counts=None, probs=None, tokens=None):
     loss = torch.empty((), dtype=torch.float32, device=dev) if loss is None else loss
     _check(loss, "loss", torch.float32, ())
     if counts is None and probs is None and tokens is None and need <= 1 << 16:
-        # one allocation, whose parts cost the host less than three more (a loss of its own: callers
-        # change it in place)
+        # one allocation, whose parts cost the host less than three more. Each part counts its own changes
+        # (.data), so that one changed in place leaves the others as autograd has saved them.
         ws, counts, tokens, probs = torch.empty(need // 4 + 2 * E + 1, dtype=torch.int32, device=dev) \
             .split_with_sizes([need // 4, E, 1, E])
-        probs = probs.view(torch.float32)
+        counts, tokens, probs = counts.data, tokens.data, probs.view(torch.float32).data
     else:
         ws = torch.empty(need // 4, dtype=torch.int32, device=dev)
         counts = _out(counts, "counts", torch.int32, (E,), dev)

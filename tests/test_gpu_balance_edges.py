@@ -64,3 +64,36 @@ def test_counts_of_many_ranks(bgt, dev, E, dtype):
     # softmax of E terms, the counts' sum and the dot product: at most 100 + E / 4 roundings to fp32
     bound = (100 + E / 4) * 2.0 ** -24 * E * p * (f + dot) + torch.finfo(dtype).eps / 2 * ref.abs() * 1.01 + torch.finfo(dtype).tiny
     assert bool(((got.double() - ref).abs() <= bound).all()) and bool(got.any())
+
+
+@pytest.mark.parametrize("T", [61, 5000])
+def test_outputs_change_in_place(bgt, dev, T):
+    """A change of one output in place leaves the others as autograd has saved them."""
+    class Loss(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, logits, ids):
+            loss, counts, probs, tokens = bgt.moe_balance(logits, ids)
+            ctx.save_for_backward(logits, counts, tokens)
+            seen.append(probs)
+            return loss
+
+        @staticmethod
+        def backward(ctx, dloss):
+            return bgt.moe_balance_backward(dloss.contiguous(), *ctx.saved_tensors), None
+
+    seen = []
+    g = torch.Generator(device=dev).manual_seed(T)
+    logits = torch.randn(T, 8, generator=g, device=dev).requires_grad_()
+    ids = torch.randint(0, 8, (T, 2), generator=g, device=dev, dtype=torch.int32)
+    Loss.apply(logits, ids).backward()
+    want = logits.grad.clone()
+    logits.grad = None
+    loss = Loss.apply(logits, ids)
+    seen[-1].mul_(0.9)                                          # a running mean, a sum over ranks
+    loss.backward()
+    assert torch.equal(logits.grad, want)
+    outs = bgt.moe_balance(logits.detach(), ids)
+    for i, t in enumerate(outs):
+        rest = [u.clone() for u in outs]
+        t.zero_()
+        assert all(torch.equal(u, v) for j, (u, v) in enumerate(zip(outs, rest)) if j != i)
