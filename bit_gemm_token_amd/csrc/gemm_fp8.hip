@@ -587,12 +587,14 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(EX
     auto step = [&](int g, uint8_t* cur, uint8_t* nxt) {
       wait_vm<0>();                                   // group g and its scales landed
       lds_barrier();                                  // ... in every wave, and nxt is read
+      asm volatile("" ::: "memory");
       take_scales();
       if (g + 1 < G) {
         scales(g + 1);
         issue(g + 1, nxt);
       }
       if (!idle) compute(cur);
+      asm volatile("" ::: "memory");                  // the reads stay ahead of their wait
       wait_lds0();
     };
 #pragma unroll 1

@@ -108,3 +108,26 @@ def test_weight_gradient_of_2_32_elements(bgt, dev, dtype):
     for k in (0, 1, 127, 12345, 32768, 65407, 65535):
         ref, size = x[:, k] @ dy.double(), x[:, k].abs() @ dy.double().abs()
         assert bool(((dw[k].double() - ref).abs() <= M * 2.0 ** -23 * size + torch.finfo(dtype).eps / 2 * ref.abs()).all())
+
+
+def whole_numbers(bgt, dev, M, K, N, dtype):
+    """Small whole numbers, whose products and sums every instruction holds: outputs are equal to the
+    sums rounded once, call after call. A row or group read too early or too late would show."""
+    g = torch.Generator(device=dev).manual_seed(M)
+    x = torch.randint(-3, 4, (M, K), generator=g, device=dev).float()
+    w = torch.randint(-3, 4, (K, N), generator=g, device=dev).float()
+    q, s = bgt.quantize_fp8(x)
+    p = bgt.pack_weights_fp8(w)
+    ref = (x.double() @ w.double()).to(dtype)
+    for _ in range(10):
+        x.zero_()                                               # other work in between
+        y = bgt.w8a8_gemm_fp8(q, s, p["qw"], p["sw"], out_dtype=dtype)
+        assert torch.equal(y, ref)
+
+
+# tiles of 64, 128 and 256; one group of K, an odd and an even number
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,K,N", [(150, 128, 500), (150, 1024, 500), (1030, 640, 3333), (1030, 768, 3333), (2048, 1024, 8200),
+                                   (2048, 384, 8200)])
+def test_whole_numbers_in_tiles(bgt, dev, dtype, M, K, N):
+    whole_numbers(bgt, dev, M, K, N, dtype)
