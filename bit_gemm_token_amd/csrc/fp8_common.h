@@ -55,6 +55,13 @@ __device__ __forceinline__ void f8_unpack4(uint32_t w, float* v) {
   v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
 }
 
+// lanes of a wave exchange through LDS: what one wrote before this the others read after it. A
+// wave's LDS accesses run in order, so this is for the compiler only.
+__device__ __forceinline__ void wave_exchange() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // stores past the L2, of outputs that nobody reads soon or that would push out what is shared
 __device__ __forceinline__ void store_once(void* p, uint4 v) {
   typedef uint32_t v4u __attribute__((ext_vector_type(4)));

@@ -248,8 +248,10 @@ __global__ __launch_bounds__(stream_waves(MT, CH) * 64) void k_f8_stream(
           *reinterpret_cast<uint4*>(mine + i * 2048 + place(8 * h + lane / 8, lane % 8)) = raw[j][i][h];
         sxb[j][i] = sraw[j][i];
       }
+      wave_exchange();
 #pragma unroll
       for (int i = 0; i < MT; ++i) xc[j][i] = read_x(mine + i * 2048);
+      wave_exchange();                                // the next group takes the same place
     }
   };
   // elements: rows 4 r + lane / 16, eight a lane, a block in 16 lanes
@@ -286,7 +288,9 @@ __global__ __launch_bounds__(stream_waves(MT, CH) * 64) void k_f8_stream(
           const uint32_t of = (uint32_t)__shfl((int)byte, c % 4 * 16, kWave);
           if (c / 4 == r) sxb[j][0] = of;
         }
+        wave_exchange();
         xc[j][0] = read_x(mine);
+        wave_exchange();
       }
     }
   };

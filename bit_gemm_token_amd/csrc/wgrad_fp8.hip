@@ -343,8 +343,7 @@ __global__ __launch_bounds__(SN * 2) __attribute__((amdgpu_waves_per_eu(2))) voi
           *reinterpret_cast<uint2*>(P + lr * 128 + ((4 * j + q) ^ (lr % 8)) * 16 + 8 * hf) =
               make_uint2(narrow2<DT>(acc[i][j][4 * q], acc[i][j][4 * q + 1]),
                          narrow2<DT>(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]));
-      wait_lds0();
-      __builtin_amdgcn_wave_barrier();
+      wave_exchange();
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const int row = 8 * t + lane / 8, c = lane % 8;
@@ -361,8 +360,7 @@ __global__ __launch_bounds__(SN * 2) __attribute__((amdgpu_waves_per_eu(2))) voi
             if (n + u < N) o[u] = e[u];
         }
       }
-      wait_lds0();
-      __builtin_amdgcn_wave_barrier();
+      wave_exchange();
     }
   }
 }

@@ -131,3 +131,34 @@ def whole_numbers(bgt, dev, M, K, N, dtype):
                                    (2048, 384, 8200)])
 def test_whole_numbers_in_tiles(bgt, dev, dtype, M, K, N):
     whole_numbers(bgt, dev, M, K, N, dtype)
+
+
+# the streaming kernel: blocks of 16, 32 and 64 rows, fewer and more groups of K than the waves keep
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,K,N", [(1, 128, 300), (5, 512, 300), (9, 4096, 300), (16, 2048, 5000), (30, 2048, 300), (32, 4096, 5000),
+                                   (64, 4096, 300), (61, 384, 9000), (16, 8192, 300), (30, 4224, 300), (61, 4608, 300)])
+def test_whole_numbers_in_few_rows(bgt, dev, M, K, N, dtype):
+    whole_numbers(bgt, dev, M, K, N, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,K,N", [(1, 512, 300), (5, 4096, 300), (8, 2048, 5000)])
+def test_whole_numbers_quantized_by_the_product(bgt, dev, M, K, N, dtype):
+    g = torch.Generator(device=dev).manual_seed(M)
+    w = torch.randint(-3, 4, (K, N), generator=g, device=dev).float()
+    p = bgt.pack_weights_fp8(w)
+    for _ in range(10):
+        x = torch.randint(-3, 4, (M, K), generator=g, device=dev).float()
+        y, q, s = bgt.w8a8_linear_fp8(x, p["qw"], p["sw"], out_dtype=dtype)
+        assert torch.equal(y, (x.double() @ w.double()).to(dtype)) and torch.equal(plain.values(q, s)[:, :K], x.double())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,K,N", [(64, 256, 256), (1000, 200, 130), (3000, 512, 2048), (600, 2048, 8192)])
+def test_whole_numbers_in_weight_gradients(bgt, dev, M, K, N, dtype):
+    g = torch.Generator(device=dev).manual_seed(M)
+    q, s = bgt.quantize_fp8(torch.randint(-3, 4, (M, K), generator=g, device=dev).float())
+    dy = torch.randint(-3, 4, (M, N), generator=g, device=dev).to(dtype)
+    ref = (plain.values(q, s)[:, :K].t() @ dy.double()).to(dtype)
+    for _ in range(5):
+        assert torch.equal(bgt.wgrad_fp8(q, s, dy, K), ref)
