@@ -908,8 +908,11 @@ def pack_weights_fp8(w, turned=False, qw=None, sw=None, qt=None, st=None):
 
 def w8a8_gemm_fp8(qx, sx, qw, sw, y=None, out_dtype=None):
     """Y = X.W of rows (quantize_fp8) and weights (pack_weights_fp8) in 8-bit floating point;
-    y (M x N) in y's dtype, else out_dtype, else float32 (float16 and bfloat16 run at the full
-    8-bit rate). With dy's codes and the turned weights (qt, st): the gradient of x."""
+    y (M x N) in y's dtype, else out_dtype, else float32. float16 and bfloat16 run at the full
+    8-bit rate; but for few rows their sums keep 13 bits below a few products' largest (off by at
+    most 2^-9 of the sum of magnitudes besides the rounding, where large products cancel too),
+    float32 outputs are sums of exact products. With dy's codes and the turned weights (qt, st):
+    the gradient of x."""
     torch = _torch()
     M, Kp = _check_rows8(qx, sx, "qx")
     N = _check_weights8(qw, sw, Kp)
@@ -921,8 +924,8 @@ def w8a8_gemm_fp8(qx, sx, qw, sw, y=None, out_dtype=None):
 
 
 def w8a8_linear_fp8(x, qw, sw, qx=None, sx=None, y=None, out_dtype=None):
-    """quantize_fp8 of x (M x K), then w8a8_gemm_fp8, y in y's dtype, else out_dtype, else x's.
-    One launch for few rows. Returns (y, qx, sx): the codes are what wgrad_fp8 takes."""
+    """quantize_fp8 of x (M x K), then w8a8_gemm_fp8, y in y's dtype, else out_dtype, else x's
+    (w8a8_gemm_fp8 says what becomes of 16-bit ones). One launch for few rows. Returns (y, qx, sx): the codes are what wgrad_fp8 takes."""
     torch = _torch()
     M, K, ld = _rows(x, "x")
     xt, dev, Kp = _elem_type(x, "x"), x.device, _padded(K)

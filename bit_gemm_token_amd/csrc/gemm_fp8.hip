@@ -5,13 +5,18 @@
 // with e4m3 codes qx (M x K'), qw (N x K') and exponent bytes a (K'/128 x M), b (K'/128 x
 // N'/128). The matrix instructions for 8-bit floats take an exponent byte for every lane's 32 k
 // of either operand, so the blocks' scales cost no vector instruction and the sums stay in
-// one fp32 accumulator. The same instruction aligns the products of a few k to the largest of
-// them and keeps 13 bits below it (measured: 2^16 + 2^3 in one group of k gives 2^16), an
-// error of about 1.4e-5 of the sum for normal data at K = 128: far below the rounding of a
-// 16-bit output, but not of an fp32 one. Outputs in fp32 therefore take bf16 products of the
-// same codes (e4m3 is exact in bf16, the products exact in fp32, four instructions in place of
-// one), with the sum of the two exponents applied to its fp32 sum at once: one alone may take the
-// sum out of range (rows of 2^118 by weights of 2^-20).
+// one fp32 accumulator. The same instruction aligns the products of eight k to the largest of them
+// and cuts off what lies more than 13 bits below that one's leading bit (measured: of 2^16 + 2^3 in
+// one group of k both are kept, + 2^2 is lost, of either sign), less than 7 * 2^-13 < 2^-10 of the
+// magnitudes that a sum adds up.
+// Measured besides the rounding: 1.8e-5 of the outputs' norm for normal rows and weights, 4.7e-5 for
+// rows with channels twenty times as large. That is a hundredth and a thirtieth of a bf16 output's
+// rounding error and a tenth and a quarter of an fp16 one's, but a sum whose large products cancel is
+// left with it, and it is too much for fp32. Outputs in fp32, and those of few rows where the stream
+// of weights hides it, therefore take bf16 products of the same codes (e4m3 is exact in bf16, the
+// products exact in fp32, four instructions in place of one), with the sum of the two exponents
+// applied to a group's fp32 sum at once: one alone may take it out of range (rows of 2^118 by weights
+// of 2^-20).
 //
 // The order of k within a group is free as long as both operands agree: a lane takes 16-byte
 // pieces where they are contiguous for its neighbours.
@@ -53,6 +58,7 @@ __device__ __forceinline__ void zero_rows(const Route& rt, int N, OutY y, int z,
     y.put(i, 0.0f);
 }
 constexpr int kZeroWgs = 64;
+constexpr int kFusedRows = 8;                         // rows quantized by the product itself
 
 // waves of a streaming workgroup at most: sixteen of 128 registers, or eight of 256 for 64 rows,
 // whose fragments take 32 registers a group, and for chunks, whose next part of x takes as many
@@ -110,15 +116,17 @@ __device__ __forceinline__ void route_block(const Route& rt, int bm, int b, int&
 // the fragments lie, took 6.2 us more than an empty launch for 64 rows x 4096 in every workgroup,
 // this 1.8) and become fragments by way of the wave's own LDS, 16-byte pieces XOR-swizzled by
 // row.
-// XT >= 0 (at most 16 rows): x comes as elements of that type and every wave turns its own
-// groups' blocks into codes (a block's scale needs no other wave); the workgroup of the first
-// item writes codes and scales out.
+// XT >= 0 (at most kFusedRows rows, CH false): x comes as elements of that type and every wave turns
+// its own groups' blocks into codes (a block's scale needs no other wave); the workgroup of the first
+// item writes codes and scales out. The elements are requested ahead of the weights and are codes by
+// the time these arrive (1 x 4096 into 4096: 7.7 us behind them).
 template <int MT, int GPW, bool CH, bool EX, int XT, bool GR>
 __global__ __launch_bounds__(stream_waves(MT, CH) * 64) void k_f8_stream(
     const void* __restrict__ x, int64_t ldx, int Kx, const uint8_t* __restrict__ sx,
     const uint8_t* __restrict__ qw, const uint8_t* __restrict__ sw, int M, int N, int K, OutY y,
     Route rt, uint8_t* __restrict__ q_out, uint8_t* __restrict__ s_out) {
   constexpr int MOST = stream_waves(MT, CH);
+  static_assert(XT < 0 || (MT == 1 && !CH), "a wave quantizes the x that it keeps");
   __shared__ float red[2][MOST * MT * 4 * 64];
   __shared__ __align__(16) uint8_t turn[MOST * MT * 2048];
   const int G = K / kGroup, B = (N + kGroup - 1) / kGroup;
@@ -187,6 +195,14 @@ __global__ __launch_bounds__(stream_waves(MT, CH) * 64) void k_f8_stream(
   uint4 wb[GPW][2], raw[GPW][MT][2];
   uint32_t sb[GPW], sxb[GPW][MT], sraw[GPW][MT];
   v8i xc[GPW][MT];
+  constexpr bool WIDE = EX && !CH && MT == 1;         // x is kept widened, before the weights arrive
+  v8b xw[WIDE ? GPW : 1][4];
+  auto widen_x = [&](int j) {
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) xw[j][u] = widen8(xc[j][0], u);
+    }
+  };
   auto load_raw = [&](int ch) {
 #pragma unroll
     for (int j = 0; j < GPW; ++j) {
@@ -222,7 +238,7 @@ __global__ __launch_bounds__(stream_waves(MT, CH) * 64) void k_f8_stream(
       wb[j][0] = *reinterpret_cast<const uint4*>(p + (int64_t)g * kGroup);
       wb[j][1] = *reinterpret_cast<const uint4*>(p + (int64_t)g * kGroup + 64);
     }
-    if constexpr (CH && XT < 0)
+    if constexpr (CH)
       if (more) load_raw(fch);
     if (CH && ++fch < chunks) return;
     fch = 0;
@@ -251,26 +267,39 @@ __global__ __launch_bounds__(stream_waves(MT, CH) * 64) void k_f8_stream(
       wave_exchange();
 #pragma unroll
       for (int i = 0; i < MT; ++i) xc[j][i] = read_x(mine + i * 2048);
+      widen_x(j);
       wave_exchange();                                // the next group takes the same place
     }
   };
   // elements: rows 4 r + lane / 16, eight a lane, a block in 16 lanes
-  auto quantize_x = [&](int ch, bool write) {
+  constexpr int XR = XT >= 0 ? kFusedRows / 4 : 1;
+  float xv[XT >= 0 ? GPW : 1][XR][8];
+  auto load_x = [&]() {
+    if constexpr (XT >= 0) {
+#pragma unroll
+      for (int j = 0; j < GPW; ++j)
+#pragma unroll
+        for (int r = 0; r < XR; ++r) {
+          const int g = j * KS + wave, row = 4 * r + s4, k = g * kGroup + 8 * c;
+#pragma unroll
+          for (int u = 0; u < 8; ++u) xv[j][r][u] = 0.0f;
+          if (row < M && g < G && k < Kx) load8<XT>(x, row * ldx + k, xv[j][r]);
+        }
+    }
+  };
+  auto quantize_x = [&](bool write) {
     if constexpr (XT >= 0) {
 #pragma unroll
       for (int j = 0; j < GPW; ++j) {
-        const int g = (ch * GPW + j) * KS + wave;
+        const int g = j * KS + wave;
         sxb[j][0] = 127;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int row = 4 * r + s4, k = g * kGroup + 8 * c;
           uint32_t byte = 127;
           uint2 q = make_uint2(0, 0);
-          if (4 * r < M) {                            // uniform
-            float v[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) v[u] = 0.0f;
-            if (row < M && g < G && k < Kx) load8<XT>(x, row * ldx + k, v);
+          if (r < XR && 4 * r < M) {                  // uniform
+            const float* const v = xv[j][r < XR ? r : 0];
             uint32_t top = 0;
 #pragma unroll
             for (int u = 0; u < 8; ++u) top = umax(top, abs_bits(v[u]));
@@ -290,18 +319,18 @@ __global__ __launch_bounds__(stream_waves(MT, CH) * 64) void k_f8_stream(
         }
         wave_exchange();
         xc[j][0] = read_x(mine);
+        widen_x(j);
         wave_exchange();
       }
     }
   };
 
   find_rows(at);
-  if constexpr (!CH && XT < 0) load_raw(0);
+  if constexpr (XT >= 0) load_x();
+  else if constexpr (!CH) load_raw(0);
   fetch();
-  if constexpr (!CH) {
-    if constexpr (XT < 0) turn_x();
-    else quantize_x(0, item == 0);
-  }
+  if constexpr (XT >= 0) quantize_x(item == 0);
+  else if constexpr (!CH) turn_x();
   const bool single = (int)blockDim.x >= MT * 256;    // an output of an item a thread at most
   int buf = 0;
   int64_t late = -1;                                  // place and value of the output to store
@@ -327,10 +356,7 @@ __global__ __launch_bounds__(stream_waves(MT, CH) * 64) void k_f8_stream(
     uint32_t worst[MT] = {};                          // of the exponent bytes: 255 makes the sum NaN
 #pragma unroll 1
     for (int ch = 0; ch < chunks; ++ch) {
-      if constexpr (CH) {
-        if constexpr (XT < 0) turn_x();
-        else quantize_x(ch, item == 0);
-      }
+      if constexpr (CH) turn_x();
 #pragma unroll
       for (int j = 0; j < GPW; ++j) {
         const v8i w = join(wb[j][0], wb[j][1]);
@@ -340,7 +366,8 @@ __global__ __launch_bounds__(stream_waves(MT, CH) * 64) void k_f8_stream(
             v4f p = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-              p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(w, u), widen8(xc[j][m], u), p, 0, 0, 0);
+              p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(w, u), WIDE ? xw[WIDE ? j : 0][u] : widen8(xc[j][m], u),
+                                                          p, 0, 0, 0);
             const int e = (int)(sxb[j][m] + sb[j]) - 254;
 #pragma unroll
             for (int r = 0; r < 4; ++r) acc[m][r] = acc[m][r] + __builtin_ldexpf(p[r], e);
@@ -705,7 +732,6 @@ hipError_t stream_t(const void* x, int64_t ldx, int64_t Kx, const uint8_t* sx, c
   return hipGetLastError();
 }
 
-constexpr int kFusedRows = 8;                         // rows quantized by the product itself
 constexpr int kStreamGroups = 32;                     // groups of K whose x the waves keep
 constexpr int kStreamRows = 64;                       // rows of a matrix that this kernel takes
 
@@ -716,18 +742,21 @@ hipError_t stream_rows(const uint8_t* qx, const uint8_t* sx, const uint8_t* qw, 
   const bool all = K <= kStreamGroups * kGroup;       // 16 waves of 2 groups, 8 of 4
   // experts' slots scatter about their mean, and one past the block reads its weights again
   if (GR) per += per / 2;
-#define BGT_STREAM(MT, GPW, CH) \
-  return stream_t<MT, GPW, CH, EX, -1, GR>(qx, K, K, sx, qw, sw, M, N, K, y, rt, nullptr, nullptr, stream, run)
+#define BGT_STREAM(MT, GPW, CH, EXACT) \
+  return stream_t<MT, GPW, CH, EXACT, -1, GR>(qx, K, K, sx, qw, sw, M, N, K, y, rt, nullptr, nullptr, stream, run)
+  // 16-bit outputs too take exact products where the weights' stream hides them (us, exact and by the
+  // 8-bit instructions): 1 / 16 / 32 rows x 4096 into 22016 20.4 / 21.8 / 25.5 and 20.7 / 22.1 / 24.7; not 61
+  // rows, 34.1 and 28.2, nor longer K, 1 x 14336 into 4096 16.9 and 15.1
   if (per <= 16) {
-    if (all) BGT_STREAM(1, 2, false);
-    BGT_STREAM(1, 2, true);
+    if (all) BGT_STREAM(1, 2, false, true);
+    BGT_STREAM(1, 2, true, EX);
   }
   if (per <= 32) {
-    if (all) BGT_STREAM(2, 2, false);
-    BGT_STREAM(2, 2, true);
+    if (all) BGT_STREAM(2, 2, false, true);
+    BGT_STREAM(2, 2, true, EX);
   }
-  if (all) BGT_STREAM(4, 4, false);
-  BGT_STREAM(4, 2, true);
+  if (all) BGT_STREAM(4, 4, false, EX);
+  BGT_STREAM(4, 2, true, EX);
 #undef BGT_STREAM
 }
 
@@ -799,10 +828,8 @@ hipError_t launch_w8a8_f8_linear(const void* x, int type, int64_t ldx, int64_t K
     if (e == hipSuccess) e = launch_f8_rows(x, type, M, Kx, ldx, q, s, stream);
     return e != hipSuccess ? e : launch_w8a8_f8(q, s, qw, sw, M, N, K, y, stream);
   }
-  const bool ex = y.type == kF32;
-#define BGT_FUSED(T)                                                                                      \
-  return ex ? stream_t<1, 2, false, true, T, false>(x, ldx, Kx, nullptr, qw, sw, M, N, K, y, rt, q, s, stream) \
-            : stream_t<1, 2, false, false, T, false>(x, ldx, Kx, nullptr, qw, sw, M, N, K, y, rt, q, s, stream)
+#define BGT_FUSED(T) \
+  return stream_t<1, 2, false, true, T, false>(x, ldx, Kx, nullptr, qw, sw, M, N, K, y, rt, q, s, stream)
   if (type == kF32) BGT_FUSED(kF32);
   if (type == kF16) BGT_FUSED(kF16);
   BGT_FUSED(kBF16);

@@ -571,10 +571,14 @@ int bgt_pack_weights_fp8(const void* w, int w_type, int64_t E, int64_t K, int64_
 /*
  * bgt_w8a8_gemm_fp8 -- y = X.W of such rows and weights, y: M x N of y_type:
  *     y_mn = sum over blocks g of 2^(a_gm + b_gn) sum_{k in g} qx_mk qw_nk
- * in fp32, rounded once. fp16 and bf16 outputs are computed by the 8-bit matrix instructions,
- * whose sums over a few k keep 13 bits below the largest product (an error of about 2^-16 of
- * the sum of magnitudes, far below the rounding); fp32 outputs from exact products, at less
- * than half the rate. For the gradient of x pass dy's codes and the turned weights (K and N
+ * in fp32, rounded once. fp32 outputs are sums of exact products, at less than half the rate.
+ * fp16 and bf16 outputs are computed by the 8-bit matrix instructions, whose sums over a few k
+ * keep 13 bits below the largest product: besides the rounding they are off by at most 2^-9 of
+ * the sum of magnitudes sum 2^(a+b) |qx qw|. For normal rows and weights that is 2e-5 of the
+ * outputs, with channels twenty times as large 5e-5 (a quarter of fp16's rounding error); where
+ * large products cancel, what is left may be lost in it. Pass an fp32 y where that matters. Up to
+ * 32 rows with K <= 4096 (of a route: rows an expert, with half as many again) are sums of exact
+ * products in every type. For the gradient of x pass dy's codes and the turned weights (K and N
  * exchanged).
  */
 int bgt_w8a8_gemm_fp8(const uint8_t* qx, const uint8_t* sx, const uint8_t* qw, const uint8_t* sw,

@@ -162,3 +162,28 @@ def test_whole_numbers_in_weight_gradients(bgt, dev, M, K, N, dtype):
     ref = (plain.values(q, s)[:, :K].t() @ dy.double()).to(dtype)
     for _ in range(5):
         assert torch.equal(bgt.wgrad_fp8(q, s, dy, K), ref)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,K,N", [(1, 256, 48), (1, 1024, 64), (8, 1024, 64), (30, 1024, 64), (60, 1024, 64), (1, 4224, 48), (20, 4224, 48),
+                                   (60, 4224, 48), (300, 1024, 200), (1100, 256, 8200)])
+def test_sums_that_cancel(bgt, dev, dtype, M, K, N):
+    """Products of 2^16 that cancel, and small ones that are left. Whole numbers, whose sums over 128 (at
+    most 2^21) and over K fp32 holds: exact products give the sums rounded once. They are fp32 outputs'
+    and those of up to 32 rows of up to 4096. The others lose of each product what lies 13 bits below
+    the largest of its group: at most 2^-9 of the magnitudes, and no better is promised."""
+    g = torch.Generator(device=dev).manual_seed(M + K)
+    x = torch.randint(-3, 4, (M, K), generator=g, device=dev).float()
+    w = torch.randint(-3, 4, (K, N), generator=g, device=dev).float()
+    x[:, 0::8], x[:, 1::8] = 256.0, -256.0
+    w[0::8] = w[1::8] = 256.0
+    q, s = bgt.quantize_fp8(x)
+    p = bgt.pack_weights_fp8(w)
+    xv, wv = plain.values(q, s), plain.matrix(p["qw"], p["sw"])
+    assert torch.equal(xv[:, :K], x.double()) and torch.equal(wv[:K], w.double())
+    y, ref = bgt.w8a8_gemm_fp8(q, s, p["qw"], p["sw"], out_dtype=dtype), xv @ wv
+    if dtype == torch.float32 or (M <= 32 and K <= 4096):
+        assert torch.equal(y, ref.to(dtype))
+    else:
+        bound = plain.product_bound(xv, wv, ref, dtype)
+        assert bool(((y.double() - ref).abs() <= bound).all()), float(((y.double() - ref).abs() / bound).max())
