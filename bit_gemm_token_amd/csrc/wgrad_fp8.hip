@@ -265,9 +265,9 @@ __global__ __launch_bounds__(SN * 2) __attribute__((amdgpu_waves_per_eu(2))) voi
     load(from + ROWS);
     load_tok(from + 2 * ROWS);
     auto step = [&](int m, const uint8_t* X, const uint8_t* Y, uint8_t* Xn, uint8_t* Yn) {
+      asm volatile("" ::: "memory");                  // the last step's reads stay ahead of their wait
       if constexpr (LOAD == kStraight) wait_vm<0>();  // step m's rows of dy landed
       wait_lds0();                                    // ... and are written
-      asm volatile("" ::: "memory");
       lds_barrier();                                  // ... in every wave, and the others are read
       asm volatile("" ::: "memory");
       issue(m + ROWS, Yn);
