@@ -226,7 +226,8 @@ __global__ __launch_bounds__(kBThreads) void k_balance_grad(
   float n = 0.0f, f[kEach];                           // n: exact up to 2^24, the counts of one call
 #pragma unroll
   for (int j = 0; j < kEach; ++j) {
-    f[j] = e0 + j < E ? (float)counts[e0 + j] : 0.0f;
+    const int c = counts[e0 + j < E ? e0 + j : E - 1]; // no branch, which would wait for each
+    f[j] = e0 + j < E ? (float)c : 0.0f;
     n += f[j];
   }
   n = group_sum<L>(n);                                // sums over many ranks may pass 2^31
