@@ -187,3 +187,25 @@ def test_sums_that_cancel(bgt, dev, dtype, M, K, N):
     else:
         bound = plain.product_bound(xv, wv, ref, dtype)
         assert bool(((y.double() - ref).abs() <= bound).all()), float(((y.double() - ref).abs() / bound).max())
+
+
+# nothing, less than a piece of 16 bytes, whole ones and odd ends; at any alignment of the elements
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,N", [(3, 1), (3, 7), (9, 333), (300, 5), (300, 1001)])
+def test_rows_behind_the_last_slot(bgt, dev, dtype, T, N):
+    """Zeros in the rows without a slot, and nothing written before or behind them."""
+    E, K = 4, 128
+    g = torch.Generator(device=dev).manual_seed(N)
+    q, s = bgt.quantize_fp8(torch.randn(T, K, generator=g, device=dev))
+    p = bgt.pack_weights_fp8(torch.randn(E, K, N, generator=g, device=dev))
+    for drop in (0.0, 0.3, 1.0):
+        offs, tok, expert = plain.route(plain.ids_of(g, T, E, 2, drop, dev), E)
+        want = None
+        for at in (8, 9, 11, 16):
+            room = torch.full((2 * T * N + 40,), 7.0, device=dev, dtype=dtype)
+            y = room[at:at + 2 * T * N].view(2 * T, N)
+            bgt.w8a8_moe_gemm_fp8(q, s, offs, tok, p["qw"], p["sw"], y=y)
+            assert not bool(y[len(expert):].ne(0).any())
+            assert bool((room[:at] == 7).all()) and bool((room[at + 2 * T * N:] == 7).all())
+            want = y.clone() if want is None else want
+            assert torch.equal(y, want)
