@@ -72,7 +72,7 @@ constexpr int kFusedRows = 8;                         // rows quantized by the p
 
 // waves of a streaming workgroup at most: sixteen of 128 registers, or eight of 256 for 64 rows,
 // whose fragments take 32 registers a group, and for chunks, whose next part of x takes as many
-// again
+// again (64 rows of exact products by expert spill 44)
 constexpr int stream_waves(int mt, bool ch) { return mt == 4 || ch ? 8 : 16; }
 
 // blocks of bm rows of all experts' slots
@@ -441,8 +441,8 @@ template <class T, class F> struct Pick<false, T, F> { using type = F; };
 // (two sets of registers), so that a group's two LDS reads and its copies run under the products;
 // its copies are 32-bit offsets from one base in scalar registers, for want of vector registers
 // (8192 x 14336 into 4096: 391 us, 425 without; 8192^3 467 and 474). Smaller tiles lose by it
-// (128 x 128, 8192^3: 576 and 532): more workgroups a CU do the same for them. fp32: eight waves of
-// at most 128 registers, so that two workgroups share a CU.
+// (128 x 128, 8192^3: 576 and 532): more workgroups a CU do the same for them. Its 256 registers
+// spill one or two. fp32: eight waves of at most 128 registers, so that two workgroups share a CU.
 template <int BN, int BM, int WN, int WM, bool EX, bool GR>
 __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(EX ? 4 : 2))) void k_f8_tile(
     const uint8_t* __restrict__ qx, const uint8_t* __restrict__ sx, const uint8_t* __restrict__ qw,
@@ -694,11 +694,13 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(EX
   __syncthreads();
   const bool vec = N % 8 == 0 && reinterpret_cast<uintptr_t>(y.p) % 16 == 0;
   uint16_t* yp = static_cast<uint16_t*>(y.p);
-  // 128 MB and more of outputs are stored past the L2 and leave the rows and weights there that tiles
-  // share (8192 x 4096 into 14336 437 us, 403 so); the next reader finds less in the caches, which
-  // costs it as much (quantizing those rows after: 500 and 498 together) or, of smaller outputs, more
-  // (4096^3: 60 and 61, together 70 and 74)
-  const bool past = (int64_t)(GR ? rt.R : M) * N >= 1 << 26;
+  // 192 MB and more of outputs are stored past the L2 and leave the rows and weights there that tiles
+  // share. The next reader then finds less in the caches, so the limit is where the two together gain
+  // (us, the product and with the quantization of its output after it, past the L2 and not): 8192 x 4096
+  // into 8192, 128 MB, 229 and 295, 248 and 284; into 11008, 172 MB, 319 and 413, 360 and 408; into 14336,
+  // 224 MB, 392 and 487, 432 and 491; into 22016, 344 MB, 602 and 761, 671 and 770; 8192 x 1024 into 14336 144
+  // and 228, 172 and 234.
+  const bool past = (int64_t)(GR ? rt.R : M) * N >= 3 << 25;
 #pragma unroll 4
   for (int t = tid; t < BM * PIECES; t += NW * 64) {
     const int r = t / PIECES, piece = t % PIECES;
@@ -722,9 +724,11 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(EX
 // ------------------------------------------------------------------ launchers
 namespace {
 
-// waves: as many as the groups; workgroups: enough for 16 waves a CU (8 for 64 rows: registers),
-// no more than items (of a route: than its slots may need). Without `run`, here and below: only whether
-// the launch is within the grid's limits.
+// waves: as many as the groups; workgroups: as many as give a CU 16 waves (8 for 64 rows: registers),
+// no more than items (of a route: than its slots may need). LDS is that of the most waves whatever
+// their number: two workgroups of 16 rows fit a CU at once, one of 32 and 64 rows, so that those of
+// few groups (below 8 and 16) follow one another with fewer waves. Without `run`, here and below: only
+// whether the launch is within the grid's limits.
 template <int MT, int GPW, bool CH, bool EX, int XT, bool GR>
 hipError_t stream_t(const void* x, int64_t ldx, int64_t Kx, const uint8_t* sx, const uint8_t* qw,
                     const uint8_t* sw, int64_t M, int64_t N, int64_t K, OutY y, const Route& rt,

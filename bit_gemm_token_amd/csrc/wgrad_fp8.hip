@@ -18,9 +18,10 @@
 //
 // What bounds it: 32 rows of a 256 x 256 tile are 1024 cycles of matrix instructions for each term
 // of dy and, for bf16, as many of LDS traffic (96 KiB read, 32 KiB written), which have to overlap.
-// 8192 rows, 4096 x 4096: bf16 240 us (1145 TFLOP/s; a library product of bf16 operands 1361), fp16
-// 437 (629, 1258 in terms), fp32 668 (411, 1234 in terms; 644 in tiles of 256 x 256). Two columns of eight
-// rows a lane, paired by byte permutes, took 390, and of 4096 rows 345 and 469 (now 232 and 381).
+// 8192 rows, 4096 x 4096: bf16 223 us back to back (1230 TFLOP/s; a library product of bf16 operands
+// 1361), fp16 415 (661, 1322 in terms), fp32 646 (425, 1276 in terms). fp32 tiles are 256 x 128, two
+// workgroups a CU: the three terms of a 256 x 256 tile leave LDS for one. Two columns of eight rows a
+// lane, paired by byte permutes, took 390, and of 4096 rows 345 and 469 (now 222 and 329-347).
 #include <algorithm>
 
 #include "fp8_common.h"
@@ -272,7 +273,7 @@ __global__ __launch_bounds__(SN * 2) __attribute__((amdgpu_waves_per_eu(2))) voi
       asm volatile("" ::: "memory");
       issue(m + ROWS, Yn);
       // a long step's codes are widened between its halves (8192 rows, 4096 x 4096 bf16: 240 us,
-      // ahead of the step 267); a short one's ahead (fp32 644 us, between 662)
+      // ahead of the step 267); a short one's ahead (fp32 646 us, between 660; fp16 415 and 424)
       constexpr int H = ROWS / 16, HALF = SK == 256 && ROWS == 64 ? H / 2 : 0;
       compute(X, Y, 0, HALF);
       put(m + ROWS, Xn, Yn);
