@@ -694,13 +694,14 @@ __global__ __launch_bounds__(WN * WM * 64) __attribute__((amdgpu_waves_per_eu(EX
   __syncthreads();
   const bool vec = N % 8 == 0 && reinterpret_cast<uintptr_t>(y.p) % 16 == 0;
   uint16_t* yp = static_cast<uint16_t*>(y.p);
-  // 192 MB and more of outputs are stored past the L2 and leave the rows and weights there that tiles
-  // share. The next reader then finds less in the caches, so the limit is where the two together gain
-  // (us, the product and with the quantization of its output after it, past the L2 and not): 8192 x 4096
-  // into 8192, 128 MB, 229 and 295, 248 and 284; into 11008, 172 MB, 319 and 413, 360 and 408; into 14336,
-  // 224 MB, 392 and 487, 432 and 491; into 22016, 344 MB, 602 and 761, 671 and 770; 8192 x 1024 into 14336 144
-  // and 228, 172 and 234.
-  const bool past = (int64_t)(GR ? rt.R : M) * N >= 3 << 25;
+  // 128 MB and more of outputs are stored past the L2 and leave the rows and weights there that tiles
+  // share. What the product gains its output's reader loses where it comes at once, and does not where
+  // other calls come first (us, past the L2 and not): 8192 x 4096 into 8192, 128 MB: the product alone 229
+  // and 248, with the quantization of its output after it 295 and 284, a feed-forward of two such
+  // products, the gate and the product back 835 and 831; into 11008, 172 MB: 319 and 360, 413 and 408, 1149
+  // and 1160; into 14336, 224 MB: 392 and 432, 487 and 491, 1391 and 1426. Below there is little either way (64
+  // MB: 117 and 117, 138 and 141).
+  const bool past = (int64_t)(GR ? rt.R : M) * N >= 1 << 26;
 #pragma unroll 4
   for (int t = tid; t < BM * PIECES; t += NW * 64) {
     const int r = t / PIECES, piece = t % PIECES;
